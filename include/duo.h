@@ -54,7 +54,8 @@ typedef enum duo_status {
     DUO_ERR_CUDA = 4,        /* a CUDA call or kernel launch failed */
     DUO_ERR_STATE = 5,       /* call not valid in the cache's current state */
     DUO_ERR_DEVICE = 6,      /* a kernel reported a device-side error (see duo_cache_error) */
-    DUO_ERR_SCRATCH_LIMIT = 7 /* the request needs more than DUO_STATIC_SCRATCH_BYTES */
+    DUO_ERR_SCRATCH_LIMIT = 7, /* the request needs more than DUO_STATIC_SCRATCH_BYTES */
+    DUO_ERR_HOST_MEMORY = 8    /* host memory ran out */
 } duo_status;
 
 /* Storage format of the retrieval heads' caches (streaming caches are always
@@ -313,6 +314,202 @@ DUO_API duo_status duo_decode_static_scratch(duo_cache* cache, int32_t layer, co
 #define DUO_ERR_BIT_PREFILL_WAIT 1u  /* duo_cache_error bits */
 #define DUO_ERR_BIT_DECODE_COPY 2u
 DUO_API duo_status duo_cache_test_wait_timeout(duo_cache* cache, int32_t launches, uint64_t timeout_ns);
+
+/* ------------------------------------------------------------------------
+ * Paged caches: many sequences of any length over one pool of pages.
+ *
+ * A duo_cache holds a fixed batch of sequences, each in a contiguous region of
+ * max_len tokens. A duo_paged cache holds up to max_seqs sequences that come,
+ * grow, branch and go: retrieval heads keep their tokens in pages of page_size
+ * rows from one pool, listed per sequence in a page table that all layers
+ * share; streaming heads keep the sink + ring window of duo_cache (same slot
+ * rule), one window per sequence. Which rows a query attends to is as in
+ * duo_prefill and duo_decode.
+ *
+ * All bookkeeping (page table, lengths, reference counts) lives in device
+ * memory and is updated by kernels: no call waits for the device or reads from
+ * it, and duo_paged_extend, _append, _prefill and _decode, captured into a CUDA
+ * graph, serve as many steps as it is replayed for.
+ *
+ * Conventions beyond those at the top of this file:
+ *  - `seqs`, `n_tok`, `row_start`, `src` and `dst` are device arrays of int32
+ *    with n entries, 0 <= n <= DUO_PAGED_MAX_BATCH (n == 0 is a no-op; row_start
+ *    has n + 1). An entry of seqs outside [0, max_seqs) is padding: it is
+ *    skipped, and its rows of the call's tensors are neither read nor written.
+ *  - One sequence may stand only once in a call's `seqs` (or `dst`); entries
+ *    that name it twice are all skipped and DUO_ERR_BIT_PAGED_ARGUMENT is set.
+ *  - What only the device can see (lengths, page numbers, duplicate entries, a
+ *    pool without enough free pages) is checked there: the call does not do
+ *    what it cannot do, as each call says, and sets bits in the cache's error
+ *    word (duo_paged_error). No page number is used before it is checked.
+ *  - Tensors are packed rows: token (or batch entry) r of q starts at
+ *    q + r * q_stride elements, its heads are contiguous; k and v share
+ *    kv_stride. A stride of 0 means dense (heads * head_dim); others are
+ *    multiples of 8 elements, at least dense and at most 2^31 - 1. */
+#define DUO_PAGED_MAX_SEQS 4096   /* sequences of one cache */
+#define DUO_PAGED_MAX_BATCH 512   /* entries of one call */
+#define DUO_PAGED_MAX_GROUP 8     /* query heads per KV head: 1 .. 8, any number */
+#define DUO_PAGED_MAX_PAGES (1 << 20)  /* pages of one pool */
+
+/* Shape of a paged cache. As duo_layout, except
+ *   max_seqs    sequences the cache can hold
+ *   page_size   tokens per page: 16, 32, 64 or 128
+ *   num_pages   pages in the pool (>= 1)
+ *   max_pages   pages of one sequence at most (the row length of the page table)
+ *   num_q_heads num_kv_heads x (1 .. DUO_PAGED_MAX_GROUP) */
+typedef struct duo_paged_layout {
+    int32_t num_layers;
+    int32_t max_seqs;
+    int32_t num_q_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t sink;
+    int32_t recent;
+    int32_t kv_format; /* DUO_KV_BF16 or DUO_KV_E4M3: storage of the pages */
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t max_pages;
+    float softmax_scale;
+} duo_paged_layout;
+
+/* Bytes of the device buffers of a paged cache (duo_paged_size). */
+typedef struct duo_paged_sizes {
+    size_t pages;      /* each of k_pages, v_pages */
+    size_t windows;    /* each of k_window, v_window */
+    size_t page_table;
+    size_t seq_len;
+    size_t page_ref;
+    size_t workspace;
+} duo_paged_sizes;
+
+/* The device buffers, owned by the caller, 256-byte aligned; a buffer of size 0
+ * may be NULL. An empty cache has seq_len and page_ref all zero; the contents of
+ * the others do not matter until they are written.
+ *   k_pages, v_pages    [num_pages][R][page_size][head_dim], R = retrieval heads
+ *                       of all layers, layer by layer in head order
+ *                       (bf16, or one-byte E4M3 codes)
+ *   k_window, v_window  [max_seqs][S][sink + recent][head_dim] bf16, S =
+ *                       streaming heads of all layers, layer by layer
+ *   page_table          int32 [max_seqs][max_pages]; the first
+ *                       ceil(seq_len / page_size) entries of a row count
+ *   seq_len             int32 [max_seqs], tokens of each sequence
+ *   page_ref            int32 [num_pages], table entries that name the page
+ *                       (0: the page is free)
+ *   workspace           scratch of the calls, the error word and the E4M3 scales */
+typedef struct duo_paged_buffers {
+    void* k_pages;
+    void* v_pages;
+    void* k_window;
+    void* v_window;
+    int32_t* page_table;
+    int32_t* seq_len;
+    int32_t* page_ref;
+    void* workspace;
+} duo_paged_buffers;
+
+/* Opaque host object: the layout, the head maps and the buffers' addresses. */
+typedef struct duo_paged duo_paged;
+
+/* duo_paged_size — bytes of each buffer (no device work). */
+DUO_API duo_status duo_paged_size(const duo_paged_layout* layout, const uint8_t* is_retrieval, duo_paged_sizes* sizes);
+
+/* duo_paged_alloc — a paged cache over the caller's buffers, on the current
+ * device. Clears the workspace on `stream` (E4M3 scales become 1) and leaves the
+ * other buffers as they are: they may already hold sequences. The caller frees
+ * the buffers after duo_paged_free. */
+DUO_API duo_status duo_paged_alloc(const duo_paged_layout* layout, const uint8_t* is_retrieval,
+                                   const duo_paged_buffers* buffers, void* stream, duo_paged** out);
+
+/* duo_paged_free — release the host object (not the buffers). NULL is allowed. */
+DUO_API duo_status duo_paged_free(duo_paged* cache);
+
+/* duo_paged_set_kv_scales — as duo_cache_set_kv_scales, for a paged cache. */
+DUO_API duo_status duo_paged_set_kv_scales(duo_paged* cache, int32_t layer, const float* k_scale,
+                                           const float* v_scale, void* stream);
+
+/* duo_paged_extend — give sequence seqs[i] n_tok[i] more tokens (1 each when
+ * n_tok is NULL): once per step, before the layers' calls. The new tokens are
+ * the last n_tok[i] positions of the sequence; their rows are written by
+ * duo_paged_append or duo_paged_decode, layer by layer.
+ * Pages are taken lowest number first, entry by entry; a last page that is only
+ * partly full and shared with other sequences (duo_paged_fork) is first replaced
+ * by a copy (all layers; when all its sharers are extended in one call, the last
+ * of them keeps the page). All or nothing: nothing changes and
+ * DUO_ERR_BIT_PAGED_CAPACITY is set when a sequence would need more than
+ * max_pages pages or the pool has too few free ones, DUO_ERR_BIT_PAGED_ARGUMENT
+ * for a negative n_tok, a sequence named twice or a length or page number out of
+ * range. */
+DUO_API duo_status duo_paged_extend(duo_paged* cache, int32_t n, const int32_t* seqs, const int32_t* n_tok,
+                                    void* stream);
+
+/* duo_paged_append — write `layer`'s rows of the newest tokens of n sequences:
+ * packed rows [row_start[i], row_start[i+1]) of k and v are the last tokens of
+ * sequence seqs[i], in order (duo_paged_extend comes first). n_rows: rows of the
+ * k and v tensors; rows outside every range are not read. Slots as in
+ * duo_cache_append. An entry whose range is not within [0, n_rows], is longer
+ * than the sequence or runs backwards is skipped (DUO_ERR_BIT_PAGED_ARGUMENT); a
+ * row that would go into a page shared with another sequence is not written
+ * (DUO_ERR_BIT_PAGED_SHARED: it would change that sequence too). */
+DUO_API duo_status duo_paged_append(duo_paged* cache, int32_t layer, int32_t n, const int32_t* seqs,
+                                    const int32_t* row_start, const void* k, const void* v, int64_t n_rows,
+                                    int64_t kv_stride, void* stream);
+
+/* duo_paged_prefill — attention of n whole prompts of `layer`, packed one behind
+ * the other: rows [row_start[i], row_start[i+1]) of q, k, v and out are prompt
+ * i, positions 0 .. ; each query attends within its own prompt (all of it up to
+ * itself in retrieval heads, sinks and window in streaming heads). Rows of
+ * another prompt or outside every range have no effect on it, whatever they
+ * hold, and out rows outside every range are not written. An empty prompt is
+ * allowed. Within a prompt a NaN or infinite v row also reaches the queries
+ * before it in the same 128-token tile. Neither reads nor changes the cache
+ * (duo_paged_append stores the rows). n_rows: rows of the tensors, below 2^30;
+ * an entry whose range is not within [0, n_rows] or runs backwards is skipped
+ * (DUO_ERR_BIT_PAGED_ARGUMENT). */
+DUO_API duo_status duo_paged_prefill(duo_paged* cache, int32_t layer, int32_t n, const int32_t* row_start,
+                                     const void* q, const void* k, const void* v, void* out, int64_t n_rows,
+                                     int64_t q_stride, int64_t kv_stride, int64_t out_stride, void* stream);
+
+/* duo_paged_decode — one decoding step of `layer` for n sequences: row i of
+ * k_new and v_new is the last token of sequence seqs[i] (duo_paged_extend comes
+ * first), at position len - 1; it is written into the sequence's page and
+ * windows, and row i of q attends to the cache with it, as in duo_decode. Row i
+ * of `out` is zero for an empty sequence. A last page that is shared is not
+ * written (DUO_ERR_BIT_PAGED_SHARED); the row's own attention still sees the new
+ * token. */
+DUO_API duo_status duo_paged_decode(duo_paged* cache, int32_t layer, int32_t n, const int32_t* seqs, const void* q,
+                                    const void* k_new, const void* v_new, void* out, int64_t q_stride,
+                                    int64_t kv_stride, int64_t out_stride, void* stream);
+
+/* duo_paged_fork — sequence dst[i], which must be empty, becomes sequence src[i]:
+ * it shares all its pages and gets a copy of its windows (all layers). One
+ * source may be forked many times in a call; a dst that stands among the src
+ * entries, is not empty or is named twice is skipped
+ * (DUO_ERR_BIT_PAGED_ARGUMENT). Fork between steps: not between duo_paged_extend
+ * and the layers' calls that write the new rows. */
+DUO_API duo_status duo_paged_fork(duo_paged* cache, int32_t n, const int32_t* src, const int32_t* dst, void* stream);
+
+/* duo_paged_copy — as duo_paged_fork, but dst[i] gets pages of its own (lowest
+ * free numbers first, entry by entry) with copies of the rows. Nothing is copied
+ * for any entry when the pool has too few free pages
+ * (DUO_ERR_BIT_PAGED_CAPACITY). */
+DUO_API duo_status duo_paged_copy(duo_paged* cache, int32_t n, const int32_t* src, const int32_t* dst, void* stream);
+
+/* duo_paged_release — sequences seqs[i] become empty; pages no other sequence
+ * names are free again. */
+DUO_API duo_status duo_paged_release(duo_paged* cache, int32_t n, const int32_t* seqs, void* stream);
+
+/* duo_paged_compact — move pages so that the ones in use are the lowest numbers:
+ * with u pages in use, those at number u and above go, in ascending order, to
+ * the free numbers below u in ascending order; the page table follows. */
+DUO_API duo_status duo_paged_compact(duo_paged* cache, void* stream);
+
+/* duo_paged_error — read and clear the cache's error word. Synchronizes `stream`
+ * (not during a capture). */
+#define DUO_ERR_BIT_PAGED_ARGUMENT 4u  /* duo_paged_error bits: an entry, length or page number out of range */
+#define DUO_ERR_BIT_PAGED_CAPACITY 8u  /* too few free pages, or more than max_pages for a sequence */
+#define DUO_ERR_BIT_PAGED_SHARED 16u   /* a write to a shared page was left out */
+#define DUO_ERR_BIT_PAGED_WAIT 32u     /* a bounded wait of a kernel ran out */
+DUO_API duo_status duo_paged_error(duo_paged* cache, void* stream, uint32_t* flags);
 
 /* duo_status_str — static description of a status code. */
 DUO_API const char* duo_status_str(duo_status status);

@@ -8,8 +8,9 @@ no fallback path.
 
 Functions keep the C names: duo_cache_alloc, duo_cache_free, duo_cache_append,
 duo_prefill, duo_decode, duo_cache_len, duo_cache_set_len, duo_cache_views,
-duo_cache_error, duo_status_str. `DuoCache` bundles a cache handle with the
-torch buffer that backs it.
+duo_cache_error, duo_status_str, the duo_paged_* calls. `DuoCache` bundles a
+cache handle with the torch buffer that backs it; `PagedCache` a paged cache
+with the torch tensors that are its pages, windows, page table and lengths.
 """
 from __future__ import annotations
 
@@ -33,6 +34,7 @@ DUO_ERR_CUDA = 4
 DUO_ERR_STATE = 5
 DUO_ERR_DEVICE = 6
 DUO_ERR_SCRATCH_LIMIT = 7
+DUO_ERR_HOST_MEMORY = 8
 DUO_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 DUO_MAX_Q_HEADS = 256
 DUO_MAX_KV_HEADS = 128
@@ -45,7 +47,17 @@ EXPORTED = ("duo_cache_alloc", "duo_cache_free", "duo_cache_append", "duo_prefil
             "duo_cache_len", "duo_cache_set_len", "duo_cache_views", "duo_cache_error", "duo_status_str",
             "duo_decode_static_scratch", "duo_cache_append_ragged", "duo_cache_seq_lens",
             "duo_cache_set_seq_lens", "duo_prefill_ragged", "duo_cache_set_kv_scales",
-            "duo_cache_test_wait_timeout")
+            "duo_cache_test_wait_timeout",
+            "duo_paged_size", "duo_paged_alloc", "duo_paged_free", "duo_paged_set_kv_scales", "duo_paged_extend",
+            "duo_paged_append", "duo_paged_prefill", "duo_paged_decode", "duo_paged_fork", "duo_paged_copy",
+            "duo_paged_release", "duo_paged_compact", "duo_paged_error")
+DUO_PAGED_MAX_SEQS = 4096  # paged caches (include/duo.h)
+DUO_PAGED_MAX_BATCH = 512
+DUO_PAGED_MAX_GROUP = 8
+DUO_ERR_BIT_PAGED_ARGUMENT = 4  # duo_paged_error bits
+DUO_ERR_BIT_PAGED_CAPACITY = 8
+DUO_ERR_BIT_PAGED_SHARED = 16
+DUO_ERR_BIT_PAGED_WAIT = 32
 DUO_TEST_WAIT_DECODE = 1  # duo_cache_test_wait_timeout kinds and duo_cache_error bits (include/duo.h)
 DUO_TEST_WAIT_PREFILL = 2
 DUO_ERR_BIT_PREFILL_WAIT = 1
@@ -57,6 +69,21 @@ class duo_layout(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("sink", ctypes.c_int32),
                 ("recent", ctypes.c_int32), ("kv_format", ctypes.c_int32), ("max_len", ctypes.c_int64),
                 ("softmax_scale", ctypes.c_float), ("reserved1", ctypes.c_int32)]
+
+
+class duo_paged_layout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_layers", "max_seqs", "num_q_heads", "num_kv_heads", "head_dim", "sink",
+                                              "recent", "kv_format", "page_size", "num_pages", "max_pages")]
+    _fields_.append(("softmax_scale", ctypes.c_float))
+
+
+class duo_paged_sizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("pages", "windows", "page_table", "seq_len", "page_ref", "workspace")]
+
+
+class duo_paged_buffers(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_window", "v_window", "page_table", "seq_len",
+                                               "page_ref", "workspace")]
 
 
 _P = ctypes.c_void_p
@@ -100,6 +127,34 @@ _lib.duo_cache_test_wait_timeout.restype = _ST
 _lib.duo_cache_test_wait_timeout.argtypes = [_P, _I32, ctypes.c_uint64]
 _lib.duo_cache_error.restype = _ST
 _lib.duo_cache_error.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint32)]
+
+_lib.duo_paged_size.restype = _ST
+_lib.duo_paged_size.argtypes = [ctypes.POINTER(duo_paged_layout), _P, ctypes.POINTER(duo_paged_sizes)]
+_lib.duo_paged_alloc.restype = _ST
+_lib.duo_paged_alloc.argtypes = [ctypes.POINTER(duo_paged_layout), _P, ctypes.POINTER(duo_paged_buffers), _P,
+                                 ctypes.POINTER(_P)]
+_lib.duo_paged_free.restype = _ST
+_lib.duo_paged_free.argtypes = [_P]
+_lib.duo_paged_set_kv_scales.restype = _ST
+_lib.duo_paged_set_kv_scales.argtypes = [_P, _I32, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float), _P]
+_lib.duo_paged_extend.restype = _ST
+_lib.duo_paged_extend.argtypes = [_P, _I32, _P, _P, _P]
+_lib.duo_paged_append.restype = _ST
+_lib.duo_paged_append.argtypes = [_P, _I32, _I32, _P, _P, _P, _P, _I64, _I64, _P]
+_lib.duo_paged_prefill.restype = _ST
+_lib.duo_paged_prefill.argtypes = [_P, _I32, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P]
+_lib.duo_paged_decode.restype = _ST
+_lib.duo_paged_decode.argtypes = [_P, _I32, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]
+_lib.duo_paged_fork.restype = _ST
+_lib.duo_paged_fork.argtypes = [_P, _I32, _P, _P, _P]
+_lib.duo_paged_copy.restype = _ST
+_lib.duo_paged_copy.argtypes = [_P, _I32, _P, _P, _P]
+_lib.duo_paged_release.restype = _ST
+_lib.duo_paged_release.argtypes = [_P, _I32, _P, _P]
+_lib.duo_paged_compact.restype = _ST
+_lib.duo_paged_compact.argtypes = [_P, _P]
+_lib.duo_paged_error.restype = _ST
+_lib.duo_paged_error.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint32)]
 
 
 class DuoError(RuntimeError):
@@ -242,6 +297,80 @@ def duo_cache_error(handle, stream=None):
     return st, f.value
 
 
+def make_paged_layout(num_layers, max_seqs, num_q_heads, num_kv_heads, head_dim, sink, recent, page_size, num_pages,
+                      max_pages, softmax_scale=0.0, kv_format=0) -> duo_paged_layout:
+    return duo_paged_layout(num_layers, max_seqs, num_q_heads, num_kv_heads, head_dim, sink, recent, kv_format, page_size,
+                            num_pages, max_pages, softmax_scale)
+
+
+def duo_paged_size(layout: duo_paged_layout, is_retrieval: Sequence[int]):
+    """(status, duo_paged_sizes): bytes of each device buffer."""
+    sizes = duo_paged_sizes()
+    st = _lib.duo_paged_size(ctypes.byref(layout), ctypes.cast(_mask_buf(is_retrieval), _P), ctypes.byref(sizes))
+    return st, sizes
+
+
+def duo_paged_alloc(layout: duo_paged_layout, is_retrieval: Sequence[int], buffers: duo_paged_buffers, stream=None):
+    """(status, handle)."""
+    handle = _P()
+    st = _lib.duo_paged_alloc(ctypes.byref(layout), ctypes.cast(_mask_buf(is_retrieval), _P), ctypes.byref(buffers),
+                              _stream(stream), ctypes.byref(handle))
+    return st, handle.value
+
+
+def duo_paged_free(handle) -> int:
+    return _lib.duo_paged_free(handle)
+
+
+def duo_paged_set_kv_scales(handle, layer, k_scale: Sequence[float], v_scale: Sequence[float], stream=None) -> int:
+    k = (ctypes.c_float * max(1, len(k_scale)))(*[float(x) for x in k_scale])
+    v = (ctypes.c_float * max(1, len(v_scale)))(*[float(x) for x in v_scale])
+    return _lib.duo_paged_set_kv_scales(handle, layer, k, v, _stream(stream))
+
+
+def duo_paged_extend(handle, n, seqs, n_tok=None, stream=None) -> int:
+    return _lib.duo_paged_extend(handle, n, _ptr(seqs), _ptr(n_tok), _stream(stream))
+
+
+def duo_paged_append(handle, layer, n, seqs, row_start, k, v, n_rows, kv_stride=0, stream=None) -> int:
+    return _lib.duo_paged_append(handle, layer, n, _ptr(seqs), _ptr(row_start), _ptr(k), _ptr(v), n_rows, kv_stride,
+                                 _stream(stream))
+
+
+def duo_paged_prefill(handle, layer, n, row_start, q, k, v, out, n_rows, q_stride=0, kv_stride=0, out_stride=0,
+                      stream=None) -> int:
+    return _lib.duo_paged_prefill(handle, layer, n, _ptr(row_start), _ptr(q), _ptr(k), _ptr(v), _ptr(out), n_rows,
+                                  q_stride, kv_stride, out_stride, _stream(stream))
+
+
+def duo_paged_decode(handle, layer, n, seqs, q, k_new, v_new, out, q_stride=0, kv_stride=0, out_stride=0,
+                     stream=None) -> int:
+    return _lib.duo_paged_decode(handle, layer, n, _ptr(seqs), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out), q_stride,
+                                 kv_stride, out_stride, _stream(stream))
+
+
+def duo_paged_fork(handle, n, src, dst, stream=None) -> int:
+    return _lib.duo_paged_fork(handle, n, _ptr(src), _ptr(dst), _stream(stream))
+
+
+def duo_paged_copy(handle, n, src, dst, stream=None) -> int:
+    return _lib.duo_paged_copy(handle, n, _ptr(src), _ptr(dst), _stream(stream))
+
+
+def duo_paged_release(handle, n, seqs, stream=None) -> int:
+    return _lib.duo_paged_release(handle, n, _ptr(seqs), _stream(stream))
+
+
+def duo_paged_compact(handle, stream=None) -> int:
+    return _lib.duo_paged_compact(handle, _stream(stream))
+
+
+def duo_paged_error(handle, stream=None):
+    f = ctypes.c_uint32(0)
+    st = _lib.duo_paged_error(handle, _stream(stream), ctypes.byref(f))
+    return st, f.value
+
+
 class DuoCache:
     """A cache handle plus the torch uint8 buffer that backs it (owned here)."""
 
@@ -328,3 +457,175 @@ class DuoCache:
 
     def set_kv_scales(self, layer, k_scale, v_scale, stream=None):
         _check(duo_cache_set_kv_scales(self.handle, layer, k_scale, v_scale, stream), "duo_cache_set_kv_scales")
+
+
+class PagedCache:
+    """A paged mixed-head cache (include/duo.h, duo_paged_*) and the tensors that hold it.
+
+    Tensors (attributes; pass `tensors`, a dict with these names, to use your own):
+      k_pages, v_pages    [num_pages, R, page_size, head_dim] bfloat16 or float8_e4m3fn, R = retrieval heads of all layers
+      k_window, v_window  [max_seqs, S, sink + recent, head_dim] bfloat16, S = streaming heads of all layers
+      page_table          int32 [max_seqs, max_pages]; seq_len int32 [max_seqs]; page_ref int32 [num_pages]
+    Sequences are numbers in [0, max_seqs), empty at first (seq_len 0). Entry lists (seqs, n_tok, row_start, src, dst)
+    are int32 tensors on the cache's device. Rows (q, k, v, out) are bfloat16 [rows, heads, head_dim]; the stride
+    between rows is free (a slice of a fused projection), a row itself is dense. A step is: extend once, then per layer
+    prefill + append (whole prompts) or decode (one token). Calls run on the current stream and must be ordered among
+    themselves; nothing waits for the device except error_flags. A captured CUDA graph of a step may be replayed.
+    """
+
+    _NAMES = ("k_pages", "v_pages", "k_window", "v_window", "page_table", "seq_len", "page_ref")
+
+    def __init__(self, num_layers, max_seqs, num_q_heads, num_kv_heads, head_dim, sink, recent, page_size, num_pages,
+                 max_pages, is_retrieval: Sequence[int], softmax_scale=0.0, kv_format=DUO_KV_BF16, device="cuda",
+                 tensors=None, stream=None):
+        import torch
+        self.handle = None
+        self.layout = make_paged_layout(num_layers, max_seqs, num_q_heads, num_kv_heads, head_dim, sink, recent, page_size,
+                                        num_pages, max_pages, softmax_scale, kv_format)
+        mask = [int(x) for x in is_retrieval]
+        if len(mask) != num_layers * num_kv_heads:
+            raise ValueError(f"is_retrieval has {len(mask)} entries, not num_layers * num_kv_heads")
+        self.is_retrieval = mask
+        st, sizes = duo_paged_size(self.layout, mask)
+        _check(st, "duo_paged_size")
+        retr = sum(mask)
+        strm = len(mask) - retr
+        page = torch.float8_e4m3fn if kv_format == DUO_KV_E4M3 else torch.bfloat16
+        shapes = {"k_pages": ((num_pages, retr, page_size, head_dim), page),
+                  "k_window": ((max_seqs, strm, sink + recent, head_dim), torch.bfloat16),
+                  "page_table": ((max_seqs, max_pages), torch.int32), "seq_len": ((max_seqs,), torch.int32),
+                  "page_ref": ((num_pages,), torch.int32)}
+        shapes["v_pages"], shapes["v_window"] = shapes["k_pages"], shapes["k_window"]
+        if tensors is None:
+            tensors = {n: torch.zeros(shapes[n][0], dtype=shapes[n][1], device=device) for n in self._NAMES}
+        self.device = tensors["seq_len"].device
+        buffers = duo_paged_buffers()
+        for n in self._NAMES:
+            t = tensors[n]
+            shape, dtype = shapes[n]
+            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{n}: expected a contiguous {dtype} tensor {shape} on {self.device}, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+            setattr(self, n, t)
+            setattr(buffers, n, t.data_ptr() or None)
+        if self.device.type != "cuda":
+            raise ValueError("a paged cache lives on a CUDA device")
+        self._workspace = torch.empty(sizes.workspace, dtype=torch.uint8, device=self.device)
+        buffers.workspace = self._workspace.data_ptr()
+        with torch.cuda.device(self.device):
+            st, handle = duo_paged_alloc(self.layout, mask, buffers, stream)
+        _check(st, "duo_paged_alloc")
+        self.handle = handle
+        self._int32, self._bf16 = torch.int32, torch.bfloat16
+
+    def close(self):
+        if getattr(self, "handle", None):
+            duo_paged_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # interpreter shutdown: module globals may already be gone
+            pass
+
+    def _entries(self, name, t, n=None):
+        if t.dtype != self._int32 or t.dim() != 1 or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name}: expected a contiguous 1-d int32 tensor on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name}: expected {n} entries, got {t.shape[0]}")
+        return t.data_ptr()
+
+    def _rows(self, name, t, heads, n=None):
+        """(address, row stride) of packed rows [n, heads, head_dim]."""
+        d = self.layout.head_dim
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype != self._bf16 or t.device != self.device:
+            raise ValueError(f"{name}: expected bfloat16 rows [*, {heads}, {d}] on {self.device}, got {t.dtype} "
+                             f"{tuple(shape)} on {t.device}")
+        if n is not None and shape[0] != n:
+            raise ValueError(f"{name}: expected {n} rows, got {shape[0]}")
+        s = t.stride()
+        if shape[0] and (s[2] != 1 or (heads > 1 and s[1] != d)):
+            raise ValueError(f"{name}: a row must be dense, got strides {s}")
+        return t.data_ptr(), (s[0] if shape[0] > 1 else 0)
+
+    def _kv(self, k, v, n):
+        heads = self.layout.num_kv_heads
+        kp, ks = self._rows("k", k, heads, n)
+        vp, vs = self._rows("v", v, heads, n)
+        if ks != vs:
+            raise ValueError(f"k and v must have the same row stride, got {ks} and {vs}")
+        return kp, vp, ks
+
+    def set_kv_scales(self, layer, k_scale, v_scale, stream=None):
+        heads = self.layout.num_kv_heads
+        if len(k_scale) != heads or len(v_scale) != heads:
+            raise ValueError(f"expected {heads} scales for k and for v")
+        _check(duo_paged_set_kv_scales(self.handle, layer, k_scale, v_scale, stream), "duo_paged_set_kv_scales")
+
+    def extend(self, seqs, n_tok=None, stream=None):
+        """Sequence seqs[i] gets n_tok[i] (default 1) more tokens."""
+        a = self._entries("seqs", seqs)
+        n = seqs.shape[0]
+        b = None if n_tok is None else self._entries("n_tok", n_tok, n)
+        _check(_lib.duo_paged_extend(self.handle, n, a, b, _stream(stream)), "duo_paged_extend")
+
+    def append(self, layer, seqs, row_start, k, v, stream=None):
+        """Rows [row_start[i], row_start[i + 1]) of k and v are the newest tokens of seqs[i]."""
+        a = self._entries("seqs", seqs)
+        n = seqs.shape[0]
+        b = self._entries("row_start", row_start, n + 1)
+        rows = k.shape[0]
+        kp, vp, ks = self._kv(k, v, rows)
+        _check(_lib.duo_paged_append(self.handle, layer, n, a, b, kp, vp, rows, ks, _stream(stream)), "duo_paged_append")
+
+    def prefill(self, layer, row_start, q, k, v, out, stream=None):
+        """Whole prompts: rows [row_start[i], row_start[i + 1]) of q, k, v and out."""
+        b = self._entries("row_start", row_start)
+        n = row_start.shape[0] - 1
+        if n < 0:
+            raise ValueError("row_start: expected one entry more than there are prompts")
+        rows, heads = q.shape[0], self.layout.num_q_heads
+        qp, qs = self._rows("q", q, heads)
+        kp, vp, ks = self._kv(k, v, rows)
+        op, os_ = self._rows("out", out, heads, rows)
+        _check(_lib.duo_paged_prefill(self.handle, layer, n, b, qp, kp, vp, op, rows, qs, ks, os_, _stream(stream)),
+               "duo_paged_prefill")
+
+    def decode(self, layer, seqs, q, k_new, v_new, out, stream=None):
+        """Row i of k_new and v_new is the newest token of seqs[i]; out[i] = attention of q[i]."""
+        a = self._entries("seqs", seqs)
+        n, heads = seqs.shape[0], self.layout.num_q_heads
+        qp, qs = self._rows("q", q, heads, n)
+        kp, vp, ks = self._kv(k_new, v_new, n)
+        op, os_ = self._rows("out", out, heads, n)
+        _check(_lib.duo_paged_decode(self.handle, layer, n, a, qp, kp, vp, op, qs, ks, os_, _stream(stream)),
+               "duo_paged_decode")
+
+    def _pairs(self, src, dst):
+        a = self._entries("src", src)
+        return src.shape[0], a, self._entries("dst", dst, src.shape[0])
+
+    def fork(self, src, dst, stream=None):
+        """Empty sequence dst[i] shares the pages of src[i]."""
+        n, a, b = self._pairs(src, dst)
+        _check(_lib.duo_paged_fork(self.handle, n, a, b, _stream(stream)), "duo_paged_fork")
+
+    def copy(self, src, dst, stream=None):
+        """Empty sequence dst[i] becomes a copy of src[i] in pages of its own."""
+        n, a, b = self._pairs(src, dst)
+        _check(_lib.duo_paged_copy(self.handle, n, a, b, _stream(stream)), "duo_paged_copy")
+
+    def release(self, seqs, stream=None):
+        a = self._entries("seqs", seqs)
+        _check(_lib.duo_paged_release(self.handle, seqs.shape[0], a, _stream(stream)), "duo_paged_release")
+
+    def compact(self, stream=None):
+        _check(_lib.duo_paged_compact(self.handle, _stream(stream)), "duo_paged_compact")
+
+    def error_flags(self, stream=None) -> int:
+        st, f = duo_paged_error(self.handle, stream)
+        _check(st, "duo_paged_error")
+        return f

@@ -7,6 +7,7 @@
 #include <new>
 
 #include "duo_internal.cuh"
+#include "paged_internal.cuh"
 
 using namespace duo;
 
@@ -139,6 +140,27 @@ bool make_chunk_map(CUtensorMap* m, const void* base, int64_t D, int64_t H, int6
     return make_map(m, base, 4, dims, strides, box);
 }
 
+}  // namespace
+
+bool duo::encode_map(CUtensorMap* m, bool bytes, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rank < 1 || rank > 5) return false;
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], e[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        e[i] = 1;
+    }
+    for (int i = 0; i < rank - 1; ++i) s[i] = strides[i];
+    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+              const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
 duo_status check_call(const duo_cache* c, int32_t layer) {
     if (!c) return DUO_ERR_INVALID_ARG;
     if (layer < 0 || layer >= c->lay.num_layers) return DUO_ERR_INVALID_ARG;
@@ -171,6 +193,7 @@ const char* duo_status_str(duo_status s) {
         case DUO_ERR_STATE: return "call not valid in the current state (device mismatch)";
         case DUO_ERR_DEVICE: return "a kernel reported a device-side error";
         case DUO_ERR_SCRATCH_LIMIT: return "request exceeds the static decode scratch (DUO_STATIC_SCRATCH_BYTES)";
+        case DUO_ERR_HOST_MEMORY: return "host memory ran out";
     }
     return "unknown status";
 }

@@ -1,0 +1,610 @@
+// prefill_packed.cu — causal attention of whole prompts packed one behind the
+// other (duo_paged_prefill), on tcgen05.
+//
+// out_i = sum_{j <= i, seen} softmax_j(scale q_i . k_j) v_j within each prompt;
+// a streaming head's query sees j < sink or i - j < recent only.
+//
+// Work item = two tiles A and B of 128 query rows that read the same K and V
+// tiles: two query heads of one KV head over the same rows (even query groups),
+// or 256 rows of one query head (odd groups). Sharing halves the K/V traffic into
+// shared memory, and the two tiles' softmax run half a step apart: while the
+// tensor core works on one tile the other's exponentials are computed. Per pair
+// of tiles and 128 keys the tensor core needs 2048 cycles (4 products of
+// 128 x 128 x D) and the 16-lane exponential unit of an SM as many, so the two
+// pipes bound the kernel together.
+//
+// One persistent CTA per SM takes items from a counter, retrieval heads first,
+// longest prompts first, last query tiles first: the long items start early and
+// the short ones fill the end. Which prompts there are is read on the device by
+// every CTA (at most 512 lengths, ranked in shared memory). Key tiles that no
+// row of the item sees are never listed: a streaming item has its sink tiles and
+// the band of its window.
+//
+// Warp roles (384 threads; registers moved from the last group to the others):
+//   warps 0-3  softmax of tile A, one thread per row    warps 4-7  of tile B
+//   warp 8     takes the items, loads Q and the K tiles (2 stages)
+//   warp 9     issues the products (one thread), owns TMEM
+//   warp 10    loads the V tiles (2 stages); in a prompt's last tile zeroes the
+//              rows behind its end, which belong to the next prompt or to nobody
+//              and may hold anything (0 x NaN would not be 0)
+// TMEM (512 columns): S of A and B, 128 columns each, P (bf16) written over the S
+// it was made from, O of A and of B at 256.
+// Softmax in the exp2 domain; the running maximum moves only when it grows by
+// more than 2^8 (exact), sums in 32 bits; P rounded to bf16, the operand type
+// (relative 2^-9 per term). Every mbarrier wait is bounded; on timeout the CTA
+// records kErrPagedWait and unwinds.
+#include "paged_internal.cuh"
+#include "prefill_common.cuh"
+
+namespace duo {
+
+namespace {
+
+constexpr int kPackThreads = 384;
+constexpr int kSoftmaxRegs = 216;
+constexpr int kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers of a 384-thread launch");
+
+// One work item, as the roles read it from the queue.
+struct PackItem {
+    int idx;            // -1: no more
+    int retr, g;        // KV head
+    int head_a, head_b; // query heads
+    int start, n;       // the prompt's first row and its rows
+    int qa, qb;         // first query row of the tiles, in the prompt
+    int na, nb;         // key tiles of A (a prefix of B's list when B exists) and B (0: no tile B)
+    int sink_tiles, band0;  // key tile j is tile j < sink_tiles ? j : band0 + j - sink_tiles
+};
+
+__device__ __forceinline__ int key_row(const PackItem& it, int j) {
+    return (j < it.sink_tiles ? j : it.band0 + j - it.sink_tiles) * kTileK;
+}
+
+template <int D>
+struct Layout {
+    static constexpr int kColBlocks = D / 64;
+    static constexpr int kTile = kColBlocks * kTileBytesPerColBlock;
+    static constexpr int kQ = 0;  // tiles A and B
+    static constexpr int kK = kQ + 2 * kTile;
+    static constexpr int kV = kK + 2 * kTile;
+    static constexpr int kBar = kV + 2 * kTile;
+    static constexpr int kQueue = kBar + 48 * 8;
+    static constexpr int kMisc = kQueue + 4 * static_cast<int>(sizeof(PackItem));
+    static constexpr int kSeqs = kMisc + 64;  // per prompt: tiles before it [n + 1], its index by rank, its length
+    static int bytes(int n) { return kSeqs + (n + 1) * 4 + n * 2 + 4 + n * 4; }
+};
+constexpr int kMaxSmem = 227 * 1024;
+
+constexpr int kQFull = 0;
+constexpr int kQEmpty = 1;
+constexpr int kKFull = 2;     // + stage
+constexpr int kKEmpty = 4;    // + stage
+constexpr int kVFull = 6;     // + stage
+constexpr int kVEmpty = 8;    // + stage
+constexpr int kVRaw = 10;     // a V tile whose tail is still to be zeroed
+constexpr int kSFull = 11;    // + tile (A, B)
+constexpr int kPFull = 13;    // + 2 tile + half: P of 64 keys written (4 arrivals)
+constexpr int kODone = 17;    // + tile, one phase per product PV
+constexpr int kOEmpty = 19;   // + tile, O read out (4 arrivals)
+constexpr int kItemFull = 21;   // + slot
+constexpr int kItemEmpty = 25;  // + slot
+constexpr int kDrain = 29;
+constexpr int kQueueSlots = 4;
+constexpr int kConsumers = 10;  // 8 softmax warps, the issuer, the V loader
+
+struct Prompts {
+    const int* tiles_before;  // by rank
+    const uint16_t* by_rank;
+    const int* len;           // by prompt
+    int n;
+};
+
+// Query tiles of a prompt of `len` rows.
+__device__ __forceinline__ int query_tiles(int len, int rows) { return (len + rows - 1) / rows; }
+
+__device__ __forceinline__ PackItem pack_item(const PackedPrefillParams& p, const Prompts& pr, int64_t idx) {
+    PackItem it;
+    const bool by_heads = (p.G & 1) == 0;       // tile pair = two heads of a group, or 256 rows of one
+    const int rows = by_heads ? kTileQ : 2 * kTileQ;
+    const int per_kv = by_heads ? p.G / 2 : p.G;
+    const int64_t n_tiles = pr.tiles_before[pr.n];
+    const int64_t of_retr = n_tiles * p.h.n_retr * per_kv;
+    it.retr = idx < of_retr;
+    const int units = (it.retr ? p.h.n_retr : p.h.n_strm) * per_kv;
+    const int64_t x = it.retr ? idx : idx - of_retr;
+    int lo = 0, up = pr.n - 1;
+    while (lo < up) {
+        const int mid = (lo + up + 1) >> 1;
+        if (static_cast<int64_t>(pr.tiles_before[mid]) * units <= x) lo = mid;
+        else up = mid - 1;
+    }
+    const int64_t y = x - static_cast<int64_t>(pr.tiles_before[lo]) * units;
+    const int nt = pr.tiles_before[lo + 1] - pr.tiles_before[lo];
+    const int qt = nt - 1 - static_cast<int>(y / units);
+    const int unit = static_cast<int>(y % units);
+    const int e = pr.by_rank[lo];
+    it.idx = 0;
+    it.g = p.h.head[(it.retr ? 0 : p.h.n_retr) + unit / per_kv];
+    it.head_a = it.g * p.G + (by_heads ? 2 * (unit % per_kv) : unit % per_kv);
+    it.head_b = by_heads ? it.head_a + 1 : it.head_a;
+    it.start = p.row_start[e];
+    it.n = pr.len[e];
+    it.qa = qt * rows;
+    it.qb = by_heads ? it.qa : it.qa + kTileQ;
+    const bool has_b = it.qb < it.n;
+    const int last_a = it.qa / kTileQ, last_b = it.qb / kTileQ;  // diagonal key tiles
+    if (it.retr) {
+        it.sink_tiles = 0;
+        it.band0 = 0;
+    } else {
+        int a = (p.S + kTileK - 1) / kTileK;
+        if (a > last_a) a = last_a;  // the band covers the rest
+        const int low = it.qa - p.R + 1;
+        const int tb = low > 0 ? low / kTileK : 0;
+        it.sink_tiles = a < tb ? a : tb;
+        it.band0 = tb;
+    }
+    it.na = it.sink_tiles + last_a - it.band0 + 1;
+    it.nb = has_b ? it.sink_tiles + last_b - it.band0 + 1 : 0;
+    return it;
+}
+
+__device__ __forceinline__ void give_up(uint32_t* err, volatile int* abort_flag) {
+    *abort_flag = 1;
+    atomicOr(err, kErrPagedWait);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPackThreads, 1)
+    prefill_packed_kernel(const __grid_constant__ PackedPrefillParams p, const __grid_constant__ PackedMaps maps) {
+    using Lay = Layout<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const uint32_t sQ = base + Lay::kQ, sK = base + Lay::kK, sV = base + Lay::kV;
+    auto bar = [&](int i) { return base + Lay::kBar + 8u * i; };
+    PackItem* queue = reinterpret_cast<PackItem*>(smem + Lay::kQueue);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Lay::kMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kMisc + 4);
+    int* tiles_before = reinterpret_cast<int*>(smem + Lay::kSeqs);
+    int* len_of = tiles_before + p.n + 1;
+    uint16_t* by_rank = reinterpret_cast<uint16_t*>(len_of + p.n);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        mbar_init(bar(kQFull), 1);
+        mbar_init(bar(kQEmpty), 1);
+        mbar_init(bar(kVRaw), 1);
+        mbar_init(bar(kDrain), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(kKFull + s), 1);
+            mbar_init(bar(kKEmpty + s), 1);
+            mbar_init(bar(kVFull + s), 1);
+            mbar_init(bar(kVEmpty + s), 1);
+            mbar_init(bar(kSFull + s), 1);
+            mbar_init(bar(kODone + s), 1);
+            mbar_init(bar(kOEmpty + s), 4);
+            mbar_init(bar(kPFull + 2 * s), 4);
+            mbar_init(bar(kPFull + 2 * s + 1), 4);
+        }
+        for (int s = 0; s < kQueueSlots; ++s) {
+            mbar_init(bar(kItemFull + s), 1);
+            mbar_init(bar(kItemEmpty + s), kConsumers);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 9) {
+        tmem_alloc(base + Lay::kMisc, kTmemCols);
+        tmem_relinquish();
+    }
+    // Prompts by length, longest first (equal ones in order), and their tiles.
+    for (int i = tid; i < p.n; i += kPackThreads) {
+        const int64_t a = p.row_start[i], b = p.row_start[i + 1];
+        const bool good = a >= 0 && b >= a && b <= p.n_rows;
+        if (!good && blockIdx.x == 0) atomicOr(p.err, kErrPagedArgument);
+        len_of[i] = good ? static_cast<int>(b - a) : 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < p.n; i += kPackThreads) {
+        const int len = len_of[i];
+        int rank = 0;
+        for (int j = 0; j < p.n; ++j) rank += len_of[j] > len || (len_of[j] == len && j < i);
+        by_rank[rank] = static_cast<uint16_t>(i);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int rows = (p.G & 1) ? 2 * kTileQ : kTileQ;
+        int sum = 0;
+        for (int i0 = 0; i0 < p.n; i0 += 32) {
+            const int i = i0 + lane;
+            const int own = i < p.n ? query_tiles(len_of[by_rank[i]], rows) : 0;
+            int t = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, t, o);
+                if (lane >= o) t += a;
+            }
+            if (i < p.n) tiles_before[i] = sum + t - own;
+            sum += __shfl_sync(0xffffffffu, t, 31);
+        }
+        if (lane == 0) tiles_before[p.n] = sum;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Prompts prompts{tiles_before, by_rank, len_of, p.n};
+    const int64_t n_items =
+        static_cast<int64_t>(tiles_before[p.n]) * (p.h.n_retr + p.h.n_strm) * ((p.G & 1) ? p.G : p.G / 2);
+
+    // Item number `ord` of this CTA; false: none left, or a wait ran out.
+    auto take_item = [&](int ord, PackItem& it) -> bool {
+        const int slot = ord % kQueueSlots;
+        if (!mbar_wait(bar(kItemFull + slot), (ord / kQueueSlots) & 1, abort_flag)) {
+            give_up(p.err, abort_flag);
+            return false;
+        }
+        it = queue[slot];
+        return it.idx >= 0;
+    };
+    auto free_item = [&](int ord) { mbar_arrive(bar(kItemEmpty + ord % kQueueSlots)); };
+
+    if (warp >= 8) {
+        regs_dec<kOtherRegs>();
+        if (warp == 8 && lane == 0) {
+            // -------------------------------------------------------- items, Q and K
+            tma_prefetch_desc(&maps.q);
+            int g = 0;  // K tiles issued
+            int q_loads = 0;
+            for (int ord = 0;; ++ord) {
+                const unsigned i = atomicAdd(p.work, 1u);
+                const bool more = i < n_items && *abort_flag == 0;
+                PackItem it;
+                it.idx = -1;
+                if (more) it = pack_item(p, prompts, i);
+                const int slot = ord % kQueueSlots;
+                if (ord >= kQueueSlots && !mbar_wait(bar(kItemEmpty + slot), ((ord / kQueueSlots) - 1) & 1, abort_flag)) {
+                    give_up(p.err, abort_flag);
+                    break;
+                }
+                queue[slot] = it;
+                mbar_arrive(bar(kItemFull + slot));
+                if (!more) break;
+                if (ord >= 1 && !mbar_wait(bar(kQEmpty), (ord - 1) & 1, abort_flag)) {
+                    give_up(p.err, abort_flag);
+                    break;
+                }
+                mbar_arrive_expect_tx(bar(kQFull), (it.nb > 0 ? 2 : 1) * Lay::kTile);
+                for (int kb = 0; kb < Lay::kColBlocks; ++kb) {
+                    tma_load_3d(sQ + kb * kTileBytesPerColBlock, &maps.q, bar(kQFull), kb * 64, it.head_a, it.start + it.qa);
+                    if (it.nb > 0)
+                        tma_load_3d(sQ + Lay::kTile + kb * kTileBytesPerColBlock, &maps.q, bar(kQFull), kb * 64, it.head_b,
+                                    it.start + it.qb);
+                }
+                q_loads = ord + 1;
+                const int n = it.na > it.nb ? it.na : it.nb;
+                bool ok = true;
+                for (int j = 0; j < n; ++j, ++g) {
+                    const int st = g & 1;
+                    if (g >= 2 && !mbar_wait(bar(kKEmpty + st), ((g >> 1) - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(bar(kKFull + st), Lay::kTile);
+                    for (int kb = 0; kb < Lay::kColBlocks; ++kb)
+                        tma_load_3d(sK + st * Lay::kTile + kb * kTileBytesPerColBlock, &maps.k, bar(kKFull + st), kb * 64,
+                                    it.g, it.start + key_row(it, j));
+                }
+                if (!ok) {
+                    give_up(p.err, abort_flag);
+                    break;
+                }
+            }
+            // Every load issued lands before the CTA may exit.
+            for (int j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_wait(bar(kKFull + (j & 1)), (j >> 1) & 1, nullptr);
+            if (q_loads > 0) mbar_wait(bar(kQFull), (q_loads - 1) & 1, nullptr);
+        } else if (warp == 10) {
+            // -------------------------------------------------------- V
+            int g = 0, raw = 0;
+            for (int ord = 0;; ++ord) {
+                PackItem it;
+                const bool more = take_item(ord, it);
+                __syncwarp();
+                if (lane == 0) free_item(ord);
+                if (!__all_sync(0xffffffffu, more)) break;
+                const int n = it.na > it.nb ? it.na : it.nb;
+                bool ok = true;
+                for (int j = 0; j < n; ++j, ++g) {
+                    const int st = g & 1;
+                    if (g >= 2 && !mbar_wait(bar(kVEmpty + st), ((g >> 1) - 1) & 1, abort_flag)) ok = false;
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const int row0 = key_row(it, j);
+                    const bool tail = row0 + kTileK > it.n;
+                    const uint32_t full = tail ? bar(kVRaw) : bar(kVFull + st);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(full, Lay::kTile);
+                        for (int kb = 0; kb < Lay::kColBlocks; ++kb)
+                            tma_load_3d(sV + st * Lay::kTile + kb * kTileBytesPerColBlock, &maps.v, full, kb * 64, it.g,
+                                        it.start + row0);
+                    }
+                    if (tail) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kVRaw), raw & 1, nullptr));
+                        ++raw;
+                        const int from = it.n - row0;
+                        for (int i = lane; i < (kTileK - from) * 8 * Lay::kColBlocks; i += 32) {
+                            const int kb = i / ((kTileK - from) * 8), k = i % ((kTileK - from) * 8);
+                            *reinterpret_cast<uint4*>(smem + Lay::kV + st * Lay::kTile + kb * kTileBytesPerColBlock +
+                                                      from * 128 + k * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kVFull + st));
+                    }
+                }
+                if (!ok) {
+                    if (lane == 0) give_up(p.err, abort_flag);
+                    break;
+                }
+            }
+            for (int j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_wait(bar(kVFull + (j & 1)), (j >> 1) & 1, abort_flag);
+        } else if (warp == 9 && lane == 0) {
+            // -------------------------------------------------------- products
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kTileK, 0, 0);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+            int g = 0;               // K/V tiles of the items before
+            int count[2] = {0, 0};   // products PV of each tile so far
+            int items[2] = {0, 0};   // items that had the tile so far
+            bool ok = true;
+            for (int ord = 0; ok; ++ord) {
+                PackItem it;
+                const bool more = take_item(ord, it);
+                free_item(ord);
+                if (!more) break;
+                const int nt[2] = {it.na, it.nb};
+                const int n = it.na > it.nb ? it.na : it.nb;
+                ok = mbar_wait(bar(kQFull), ord & 1, abort_flag);
+                int k_ready = 0, v_ready = 0;
+                // S(x) = Q(x) K(j)^T
+                auto qk = [&](int x, int j) {
+                    const int st = (g + j) & 1;
+                    if (k_ready <= j) {
+                        if (!mbar_wait(bar(kKFull + st), ((g + j) >> 1) & 1, abort_flag)) return false;
+                        k_ready = j + 1;
+                    }
+                    tc_fence_after();
+                    const uint32_t q = sQ + x * Lay::kTile, k = sK + st * Lay::kTile;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kTileBytesPerColBlock + (kk & 3) * 32;
+                        tc_mma_ss(tmem + x * kTileK, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024),
+                                  idesc_qk, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(bar(kSFull + x));
+                    if (x == 1 || j >= nt[1]) {  // the last to read the tile
+                        tc_commit(bar(kKEmpty + st));
+                        if (j + 1 == n) tc_commit(bar(kQEmpty));
+                    }
+                    return true;
+                };
+                // O(x) += P(x) V(j)
+                auto pv = [&](int x, int j) {
+                    const int st = (g + j) & 1;
+                    if (v_ready <= j) {
+                        if (!mbar_wait(bar(kVFull + st), ((g + j) >> 1) & 1, abort_flag)) return false;
+                        v_ready = j + 1;
+                    }
+                    if (j == 0 && items[x] > 0 && !mbar_wait(bar(kOEmpty + x), (items[x] - 1) & 1, abort_flag)) return false;
+                    const uint32_t vt = sV + st * Lay::kTile;
+                    for (int half = 0; half < 2; ++half) {
+                        if (!mbar_wait(bar(kPFull + 2 * x + half), count[x] & 1, abort_flag)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const int kk = half * 4 + k4;
+                            tc_mma_ts(tmem + kTmemO + x * 128, tmem + x * kTileK + kk * 8,
+                                      smem_desc_sw128(vt + kk * 2048, kTileBytesPerColBlock, 1024), idesc_pv,
+                                      (j > 0 || kk > 0) ? 1u : 0u);
+                        }
+                    }
+                    tc_commit(bar(kODone + x));
+                    if (x == 1 || j >= nt[1]) tc_commit(bar(kVEmpty + st));
+                    ++count[x];
+                    return true;
+                };
+                for (int x = 0; ok && x < 2; ++x)
+                    if (nt[x] > 0) ok = qk(x, 0);
+                for (int j = 0; ok && j < n; ++j)
+                    for (int x = 0; ok && x < 2; ++x) {
+                        if (j >= nt[x]) continue;
+                        ok = pv(x, j);
+                        if (ok && j + 1 < nt[x]) ok = qk(x, j + 1);
+                    }
+                for (int x = 0; x < 2; ++x) items[x] += nt[x] > 0;
+                g += n;
+            }
+            if (!ok) give_up(p.err, abort_flag);
+            tc_commit(bar(kDrain));  // every product issued has completed before TMEM is released
+            mbar_wait(bar(kDrain), 0, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        regs_inc<kSoftmaxRegs>();
+        const int x = warp >> 2;  // tile
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_base + x * kTileK;
+        const uint32_t tO = tmem + lane_base + kTmemO + x * 128;
+        const uint64_t scale2 = f2pack(p.scale_log2, p.scale_log2);
+        int count = 0;  // key tiles so far
+        bool ok = true;
+        for (int ord = 0; ok; ++ord) {
+            PackItem it;
+            const bool more = take_item(ord, it);
+            __syncwarp();
+            if (lane == 0) free_item(ord);
+            if (!__all_sync(0xffffffffu, more)) break;
+            const int n = x ? it.nb : it.na;
+            if (n == 0) continue;
+            const int q0 = x ? it.qb : it.qa;
+            const int head = x ? it.head_b : it.head_a;
+            const RowVis vis = row_visible(it.retr, 0, it.n, p.S, p.R, q0 + row);
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < n; ++j, ++count) {
+                if (!__all_sync(0xffffffffu, mbar_wait(bar(kSFull + x), count & 1, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+                tc_wait_ld();
+                const int row0 = key_row(it, j);
+                const bool full = row0 + kTileK <= q0 && (it.retr || row0 + kTileK <= p.S || row0 > q0 + kTileQ - 1 - p.R);
+                if (!full) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t bits = chunk_bits_row(vis, row0 + 32 * c);
+                        if (!__all_sync(0xffffffffu, bits == 0xFFFFFFFFu)) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((bits >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
+                        }
+                    }
+                }
+                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+                const float mt = fmax3(fmaxf(m[0], m[1]), m[2], m[3]) * p.scale_log2;
+                float factor = 1.f;
+                if (mt > m_run + kRescaleThreshold) {
+                    factor = fast_exp2(m_run - mt);
+                    m_run = mt;
+                }
+                // PV(j-1) is the last product that wrote O.
+                if (j >= 1 && __any_sync(0xffffffffu, factor != 1.f)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone + x), (count - 1) & 1, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t r[16];
+                        tmem_ld16(tO + c * 16, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * factor);
+                        tmem_st16(tO + c * 16, r);
+                    }
+                }
+                const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                const uint64_t negm = f2pack(-m_use, -m_use);
+                uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        float e0, e1;
+                        f2unpack(ffma2(f2pack(__uint_as_float(s[2 * h + (i >> 5)][i & 31]),
+                                              __uint_as_float(s[2 * h + (i >> 5)][(i & 31) + 1])),
+                                       scale2, negm),
+                                 e0, e1);
+                        const float p0 = fast_exp2(e0), p1 = fast_exp2(e1);
+                        acc[(i >> 1) & 1] = fadd2(acc[(i >> 1) & 1], f2pack(p0, p1));
+                        pk[i >> 1] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st32(tS + h * 32, pk);  // every S column has been read
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kPFull + 2 * x + h));
+                }
+                float a0, a1;
+                f2unpack(fadd2(acc[0], acc[1]), a0, a1);
+                l_run = l_run * factor + (a0 + a1);
+            }
+            if (!ok) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone + x), (count - 1) & 1, abort_flag))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float inv = 1.f / l_run;
+            const bool store = q0 + row < it.n;
+            bf16* o = p.out + (static_cast<int64_t>(it.start) + q0 + row) * p.out_stride + head * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
+                tmem_ld32(tO + c * 32, r);
+                tc_wait_ld();
+                if (c + 1 == D / 32) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kOEmpty + x));
+                }
+                if (store) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint4 w;
+                        w.x = pack_bf16x2(__uint_as_float(r[i]) * inv, __uint_as_float(r[i + 1]) * inv);
+                        w.y = pack_bf16x2(__uint_as_float(r[i + 2]) * inv, __uint_as_float(r[i + 3]) * inv);
+                        w.z = pack_bf16x2(__uint_as_float(r[i + 4]) * inv, __uint_as_float(r[i + 5]) * inv);
+                        w.w = pack_bf16x2(__uint_as_float(r[i + 6]) * inv, __uint_as_float(r[i + 7]) * inv);
+                        *reinterpret_cast<uint4*>(o + c * 32 + i) = w;
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up(p.err, abort_flag);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+    if (tid == 0) {  // the last CTA leaves the counters at zero for the next launch
+        const uint32_t done = atomicAdd(p.work + 1, 1u);
+        if (done == gridDim.x - 1) {
+            p.work[0] = 0u;
+            p.work[1] = 0u;
+        }
+    }
+}
+
+template <int D>
+cudaError_t launch_d(const PackedPrefillParams& p, const PackedMaps& m, int num_sms, cudaStream_t s) {
+    static SmemLimitOnce limit;
+    const cudaError_t e = limit.apply(reinterpret_cast<const void*>(&prefill_packed_kernel<D>), kMaxSmem);
+    if (e != cudaSuccess) return e;
+    // The whole shared memory for every D: one CTA per SM, so none waits for TMEM.
+    prefill_packed_kernel<D><<<static_cast<unsigned>(num_sms), kPackThreads, kMaxSmem, s>>>(p, m);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_packed(const PackedPrefillParams& p, const PackedMaps& m, int num_sms, cudaStream_t s) {
+    if (Layout<128>::bytes(p.n) > kMaxSmem) return cudaErrorInvalidValue;
+    return p.D == 128 ? launch_d<128>(p, m, num_sms, s) : launch_d<64>(p, m, num_sms, s);
+}
+
+}  // namespace duo

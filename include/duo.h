@@ -355,7 +355,8 @@ DUO_API duo_status duo_cache_test_wait_timeout(duo_cache* cache, int32_t launche
  *   max_seqs    sequences the cache can hold
  *   page_size   tokens per page: 16, 32, 64 or 128
  *   num_pages   pages in the pool (>= 1)
- *   max_pages   pages of one sequence at most (the row length of the page table)
+ *   max_pages   pages of one sequence at most (the row length of the page table);
+ *               max_pages x page_size <= 2^27
  *   num_q_heads num_kv_heads x (1 .. DUO_PAGED_MAX_GROUP) */
 typedef struct duo_paged_layout {
     int32_t num_layers;
@@ -508,7 +509,8 @@ DUO_API duo_status duo_paged_compact(duo_paged* cache, void* stream);
 #define DUO_ERR_BIT_PAGED_ARGUMENT 4u  /* duo_paged_error bits: an entry, length or page number out of range */
 #define DUO_ERR_BIT_PAGED_CAPACITY 8u  /* too few free pages, or more than max_pages for a sequence */
 #define DUO_ERR_BIT_PAGED_SHARED 16u   /* a write to a shared page was left out */
-#define DUO_ERR_BIT_PAGED_WAIT 32u     /* a bounded wait of a kernel ran out */
+#define DUO_ERR_BIT_PAGED_WAIT 32u     /* a bounded wait of a kernel ran out: the outputs since then are not
+                                        * valid, and a new duo_paged over the same buffers is needed */
 DUO_API duo_status duo_paged_error(duo_paged* cache, void* stream, uint32_t* flags);
 
 /* duo_status_str — static description of a status code. */

@@ -516,7 +516,15 @@ class PagedCache:
             st, handle = duo_paged_alloc(self.layout, mask, buffers, stream)
         _check(st, "duo_paged_alloc")
         self.handle = handle
+        self._constants()
+
+    def _constants(self):
+        """What the argument checks compare with on every call."""
+        import torch
         self._int32, self._bf16 = torch.int32, torch.bfloat16
+        self._index = -1 if self.device.type == "cpu" else self.device.index
+        self._dim, self._q_heads, self._kv_heads = (self.layout.head_dim, self.layout.num_q_heads,
+                                                    self.layout.num_kv_heads)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -530,7 +538,7 @@ class PagedCache:
             pass
 
     def _entries(self, name, t, n=None):
-        if t.dtype != self._int32 or t.dim() != 1 or not t.is_contiguous() or t.device != self.device:
+        if t.dtype is not self._int32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != self._index:
             raise ValueError(f"{name}: expected a contiguous 1-d int32 tensor on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
         if n is not None and t.shape[0] != n:
@@ -539,20 +547,21 @@ class PagedCache:
 
     def _rows(self, name, t, heads, n=None):
         """(address, row stride) of packed rows [n, heads, head_dim]."""
-        d = self.layout.head_dim
+        d = self._dim
         shape = t.shape
-        if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype != self._bf16 or t.device != self.device:
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype is not self._bf16 or t.get_device() != self._index:
             raise ValueError(f"{name}: expected bfloat16 rows [*, {heads}, {d}] on {self.device}, got {t.dtype} "
                              f"{tuple(shape)} on {t.device}")
-        if n is not None and shape[0] != n:
-            raise ValueError(f"{name}: expected {n} rows, got {shape[0]}")
+        rows = shape[0]
+        if n is not None and rows != n:
+            raise ValueError(f"{name}: expected {n} rows, got {rows}")
         s = t.stride()
-        if shape[0] and (s[2] != 1 or (heads > 1 and s[1] != d)):
+        if rows and (s[2] != 1 or (heads > 1 and s[1] != d)):
             raise ValueError(f"{name}: a row must be dense, got strides {s}")
-        return t.data_ptr(), (s[0] if shape[0] > 1 else 0)
+        return t.data_ptr(), (s[0] if rows > 1 else 0)
 
     def _kv(self, k, v, n):
-        heads = self.layout.num_kv_heads
+        heads = self._kv_heads
         kp, ks = self._rows("k", k, heads, n)
         vp, vs = self._rows("v", v, heads, n)
         if ks != vs:
@@ -587,7 +596,7 @@ class PagedCache:
         n = row_start.shape[0] - 1
         if n < 0:
             raise ValueError("row_start: expected one entry more than there are prompts")
-        rows, heads = q.shape[0], self.layout.num_q_heads
+        rows, heads = q.shape[0], self._q_heads
         qp, qs = self._rows("q", q, heads)
         kp, vp, ks = self._kv(k, v, rows)
         op, os_ = self._rows("out", out, heads, rows)
@@ -597,7 +606,7 @@ class PagedCache:
     def decode(self, layer, seqs, q, k_new, v_new, out, stream=None):
         """Row i of k_new and v_new is the newest token of seqs[i]; out[i] = attention of q[i]."""
         a = self._entries("seqs", seqs)
-        n, heads = seqs.shape[0], self.layout.num_q_heads
+        n, heads = seqs.shape[0], self._q_heads
         qp, qs = self._rows("q", q, heads, n)
         kp, vp, ks = self._kv(k_new, v_new, n)
         op, os_ = self._rows("out", out, heads, n)

@@ -51,7 +51,7 @@ duo_status check_layout(const duo_paged_layout* L, const uint8_t* mask, int64_t*
     if (L->page_size != 16 && L->page_size != 32 && L->page_size != 64 && L->page_size != 128)
         return DUO_ERR_INVALID_ARG;
     if (L->num_pages < 1 || L->num_pages > DUO_PAGED_MAX_PAGES) return DUO_ERR_INVALID_ARG;
-    if (L->max_pages < 1 || static_cast<int64_t>(L->max_pages) * L->page_size > (1 << 30)) return DUO_ERR_INVALID_ARG;
+    if (L->max_pages < 1 || static_cast<int64_t>(L->max_pages) * L->page_size > (1 << 27)) return DUO_ERR_INVALID_ARG;
     if (!(L->softmax_scale >= 0.f) || !std::isfinite(L->softmax_scale)) return DUO_ERR_INVALID_ARG;
     const int64_t n = static_cast<int64_t>(L->num_layers) * L->num_kv_heads;
     int64_t r = 0;
@@ -203,6 +203,7 @@ duo_status duo_paged_alloc(const duo_paged_layout* layout, const uint8_t* is_ret
     v.r_all = static_cast<int32_t>(nr);
     v.s_all = static_cast<int32_t>(ns);
     v.elem = c->fp8 ? 1 : 2;
+    for (v.P_log2 = 4; (1 << v.P_log2) < v.P;) ++v.P_log2;
     int32_t r0 = 0, s0 = 0;
     for (int32_t l = 0; l < L.num_layers; ++l) {
         PagedHeads& h = c->heads[l];

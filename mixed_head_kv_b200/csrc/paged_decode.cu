@@ -52,24 +52,6 @@ constexpr int kMaxG = DUO_PAGED_MAX_GROUP;
 // of each part in one CTA.
 constexpr int kPartsPerPair = 48;
 
-template <int D>
-struct Smem {
-    static constexpr int kStage = D * 256;  // K and V of a tile
-    static constexpr int kStages = kRingBytes / kStage;
-    static constexpr int kRing = 0;
-    static constexpr int kQSlot = (kMaxG + 2) * D * 2;  // queries, new K row, new V row
-    static constexpr int kQ = kRing + kRingBytes;
-    static constexpr int kMerge = kQ + 2 * kQSlot;      // one warp's O
-    static constexpr int kStat = kMerge + kMaxG * D * 4;  // maximum and sum of a warp's heads
-    static constexpr int kBar = kStat + kWarps * kMaxG * 2 * 4;
-    static constexpr int kMisc = kBar + 32 * 8;
-    static constexpr int kPrefix = kMisc + 32;  // per entry: length, tiles before (retrieval, streaming), sequence
-};
-__host__ __device__ constexpr int smem_bytes(int D, int n) {
-    return (D == 128 ? Smem<128>::kPrefix : Smem<64>::kPrefix) + (n + 1) * 8 + n * 4 + n * 2 + 8;
-}
-static_assert(smem_bytes(128, kPagedMaxBatch) <= 113 * 1024, "two CTAs per SM");
-
 constexpr int kFull = 0;     // + stage (up to 6)
 constexpr int kEmpty = 6;    // + stage
 constexpr int kQFull = 12;   // + slot
@@ -119,24 +101,135 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint4& x) {
 // The computing warps' barrier.
 __device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+__device__ __forceinline__ bool group_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return r != 0u;
+}
+
+// The sums over the warps of accumulators [W n, W n + n), n = steps / 4, in warp W.
+// In round i a warp hands its part of quarter W + i over: 4 KB serve all.
+template <int W, int kSteps>
+__device__ __forceinline__ void gather_quarter(const float (&o)[kSteps][4], float (&r)[kSteps / kWarps][4], float* merge,
+                                               int lane) {
+    constexpr int n = kSteps / kWarps;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[i][j] = o[W * n + i][j];
+#pragma unroll
+    for (int t = 1; t < kWarps; ++t) {
+        constexpr int mask = kWarps - 1;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const int k = ((W + t) & mask) * n + i;
+            *reinterpret_cast<float4*>(merge + (k * 32 + lane) * 4) = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
+        }
+        group_sync();
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float4 y = *reinterpret_cast<const float4*>(merge + ((W * n + i) * 32 + lane) * 4);
+            r[i][0] += y.x;
+            r[i][1] += y.y;
+            r[i][2] += y.z;
+            r[i][3] += y.w;
+        }
+        if (t + 1 < kWarps) group_sync();
+    }
+}
+
 // One stretch of tiles of one (entry, KV head) pair inside a CTA's share.
 struct Segment {
     int e, seq, len;     // entry, sequence, its tokens
     int idx;             // index of the head in the layer's list (retrieval first)
     int retr;            // 1: pages, 0: window
     int t0, t1, tiles;   // tiles [t0, t1) of `tiles`
-    int64_t first;       // number of the pair's first tile in the whole list
+    int units;           // units of the list it takes up
+    int new_row;         // the new token's row in the pages' list or the window
+    int parts;           // shares that hold tiles of the pair
+    int part0;           // slot of the first share's part; those of the others follow, two apart from 2 (share + 1)
 };
 
+template <int D>
+struct Smem {
+    static constexpr int kStage = D * 256;  // K and V of a tile
+    static constexpr int kStages = kRingBytes / kStage;
+    static constexpr int kRing = 0;
+    static constexpr int kQSlot = (kMaxG + 2) * D * 2;  // queries, new K row, new V row
+    static constexpr int kQ = kRing + kRingBytes;
+    static constexpr int kMerge = kQ + 2 * kQSlot;      // one warp's O
+    static constexpr int kStat = kMerge + kMaxG * D * 4;  // maximum and sum of a warp's heads
+    static constexpr int kBar = kStat + kWarps * kMaxG * 2 * 4;
+    static constexpr int kMisc = kBar + 32 * 8;
+    static constexpr int kSeg = kMisc + 16;     // the two segments in flight, and two cut pairs to be joined
+    static constexpr int kHeads = kSeg + 4 * static_cast<int>(sizeof(Segment));  // the layer's KV heads
+    static constexpr int kPrefix = kHeads + DUO_MAX_KV_HEADS * 2;  // per entry: length, tiles before (retrieval, streaming), sequence
+};
+__host__ __device__ constexpr int smem_bytes(int D, int n) {
+    return (D == 128 ? Smem<128>::kPrefix : Smem<64>::kPrefix) + (n + 1) * 8 + n * 4 + n * 2 + 8;
+}
+static_assert(smem_bytes(128, kPagedMaxBatch) <= 113 * 1024, "two CTAs per SM");
+
+// Division, one copy for the whole kernel: most of its code is run once per CTA, and
+// what runs once waits for the instruction cache line by line.
+__device__ __noinline__ int64_t divide(int64_t a, int64_t b) {  // both >= 0, b > 0
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// T units over n CTAs: the first `more` shares hold `base` + 1 units, the others `base`.
+struct Shares {
+    int64_t base;
+    int more;
+    __device__ __forceinline__ int64_t start(int c) const { return base * c + (c < more ? c : more); }
+    __device__ __forceinline__ int of(int64_t u) const {
+        const int64_t large = (base + 1) * more;
+        return u < large ? static_cast<int>(divide(u, base + 1)) : more + static_cast<int>(divide(u - large, base));
+    }
+};
+
+// The list of work: units are the tiles of a pair and one more for its end (joining
+// the warps and writing the result takes about as long as a tile), so that shares
+// of many short pairs weigh as much as shares of long ones.
 struct Work {
     const int* len;
-    const int* before_r;  // [n + 1] retrieval tiles of one head before entry i
+    const int* before_r;  // [n + 1] units of one retrieval head before entry i
     const int* before_s;
     const uint16_t* seq;
     int n, n_retr, n_strm;
-    int64_t of_retr, total;
+    int64_t of_retr;
+    Shares shares;
+    int c;                // this CTA's share
 
-    // The segment that starts at tile u and ends at `hi` at the latest.
+    // Unit `at` of the pair is unit u of the list; `n` units in the pair.
+    __device__ __forceinline__ void fill(Segment& s, int n, int at, int64_t u, int64_t hi) const {
+        const int64_t left = hi - u;
+        const int end = left < n - at ? at + static_cast<int>(left) : n;
+        s.tiles = n - 1;
+        s.units = end - at;
+        s.t0 = at < s.tiles ? at : s.tiles;
+        s.t1 = end < s.tiles ? end : s.tiles;
+        s.seq = seq[s.e];
+        s.len = len[s.e];
+    }
+    // Where the parts of the pair are, for a segment that starts at unit u and has tiles.
+    __device__ __forceinline__ void find_parts(Segment& s, int64_t u) const {
+        s.parts = 1;
+        s.part0 = 0;
+        if (s.t1 - s.t0 < s.tiles) {
+            const int64_t first = u - s.t0;
+            const int c0 = s.t0 == 0 ? c : shares.of(first);
+            const int c1 = s.t1 == s.tiles ? c : shares.of(first + s.tiles - 1);
+            s.parts = c1 - c0 + 1;
+            // A share has two slots: 2 c for the pair that it begins in, 2 c + 1 for the one that it ends in.
+            s.part0 = 2 * c0 + (first > shares.start(c0) ? 1 : 0);
+        }
+    }
+    // The segment that starts at unit u and ends at `hi` at the latest.
     __device__ __forceinline__ Segment at(int64_t u, int64_t hi) const {
         Segment s;
         s.retr = u < of_retr;
@@ -150,30 +243,117 @@ struct Work {
             else up = mid - 1;
         }
         s.e = lo;
-        s.tiles = before[lo + 1] - before[lo];
+        const int units = before[lo + 1] - before[lo];
         const int64_t y = x - static_cast<int64_t>(before[lo]) * heads;
-        const int h = static_cast<int>(y / s.tiles);
-        s.t0 = static_cast<int>(y - static_cast<int64_t>(h) * s.tiles);
-        s.first = u - s.t0;
-        const int64_t left = hi - u;
-        s.t1 = left < s.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.tiles;
+        const int h = static_cast<int>(divide(y, units));
         s.idx = s.retr ? h : n_retr + h;
-        s.seq = seq[lo];
-        s.len = len[lo];
+        fill(s, units, static_cast<int>(y - static_cast<int64_t>(h) * units), u, hi);
         return s;
     }
+    // The one behind it, which starts at unit u: the next head, or the next entry
+    // with rows, or the first of the windows.
+    __device__ __forceinline__ void next(Segment& s, int64_t u, int64_t hi) const {
+        int units = s.tiles + 1;
+        ++s.idx;
+        if (s.idx == (s.retr ? n_retr : n_retr + n_strm)) {
+            if (u == of_retr) {
+                s.retr = 0;
+                s.e = -1;
+            }
+            const int* before = s.retr ? before_r : before_s;
+            do {
+                ++s.e;
+                units = before[s.e + 1] - before[s.e];
+            } while (units == 0);
+            s.idx = s.retr ? 0 : n_retr;
+        }
+        fill(s, units, 0, u, hi);
+    }
 };
-
-__device__ __forceinline__ int64_t share_start(int64_t total, int c, int n) { return total * c / n; }
-__device__ __forceinline__ int share_of(int64_t total, int64_t u, int n) {
-    return static_cast<int>(((u + 1) * n - 1) / total);
-}
 
 __device__ __forceinline__ void report(uint32_t* err, uint32_t bit) { atomicOr(err, bit); }
 
 // The window row of position pos.
 __device__ __forceinline__ int window_slot(const PagedView& v, int pos) {
     return pos < v.S ? pos : v.S + (pos - v.S) % v.R;
+}
+
+// Joins the parts of a cut pair into its G output rows. A warp takes a head (with
+// fewer than four heads, the parts of a head are shared out between warps): its
+// lanes read the parts' statistics at once, D / 32 columns each of eight parts at a
+// time. The first eight are on their way before the statistics that weigh them.
+template <int D>
+__device__ __forceinline__ void join_parts(const PagedDecodeParams& p, const Segment& s, int g, float v_scale, float* merge,
+                                           int warp, int lane) {
+    constexpr int V = D / 32, B = 8;  // columns per lane, parts per batch
+    const int n = s.parts;
+    const int split = p.G == 1 ? kWarps : p.G == 2 ? kWarps / 2 : 1;  // warps per head
+    const int sub = warp & (split - 1);
+    // Part k is in slot part0 for k = 0, else in slot 2 (c0 + k).
+    const int even = s.part0 & ~1;
+    for (int h0 = 0; h0 < p.G; h0 += kWarps / split) {
+        const int h = h0 + warp / split;
+        const bool on = h < p.G;  // else the warp works on head 0 and keeps it to itself
+        const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + (on ? h : 0);
+        const float* po = p.part_o + (on ? h : 0) * D + lane * V;
+        float m = -INFINITY, sum = 0.f, w = 0.f, acc[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < n; c += 32) {  // 32 parts with their weights one per lane
+#pragma unroll 1
+            for (int k0 = c + sub; k0 < n && k0 < c + 32; k0 += B * split) {
+                float x[B][V];
+#pragma unroll
+                for (int j = 0; j < B; ++j) {
+                    const int k = k0 + j * split;
+                    const float* src = po + static_cast<int64_t>((k == 0 || k >= n ? s.part0 : even + 2 * k) * p.G) * D;
+                    if (V == 4) *reinterpret_cast<float4*>(x[j]) = __ldcg(reinterpret_cast<const float4*>(src));
+                    else *reinterpret_cast<float2*>(x[j]) = __ldcg(reinterpret_cast<const float2*>(src));
+                }
+                if (k0 == c + sub) {
+                    auto stat_of = [&](int k) {
+                        return k < n ? __ldcg(ml + (k == 0 ? s.part0 : even + 2 * k) * p.G) : make_float2(-INFINITY, 0.f);
+                    };
+                    if (c == 0) {  // the joint maximum
+#pragma unroll 1
+                        for (int k = 0; k < n; k += 32) m = fmaxf(m, stat_of(k + lane).x);
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                    }
+                    const float2 y = stat_of(c + lane);
+                    w = y.x == m ? 1.f : fast_exp2(y.x - m);
+                    sum += y.y * w;  // (used by the head's first warp, which has a part of every batch)
+                }
+#pragma unroll
+                for (int j = 0; j < B; ++j) {
+                    const int k = k0 + j * split;
+                    const float f = __shfl_sync(0xffffffffu, w, k & 31);
+                    if (k < n && k < c + 32)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) acc[v] += x[j][v] * f;
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (split > 1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) merge[(warp * V + v) * 32 + lane] = acc[v];
+            group_sync();
+            if (sub == 0)
+#pragma unroll 1
+                for (int o = 1; o < split; ++o)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[v] += merge[((warp + o) * V + v) * 32 + lane];
+        }
+        if (on && sub == 0) {
+            const float f = v_scale / sum;
+            bf16* dst = p.out + s.e * p.out_stride + (g * p.G + h) * D + lane * V;
+#pragma unroll
+            for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(dst + v) = pack_bf16x2(acc[v] * f, acc[v + 1] * f);
+        }
+    }
 }
 
 template <int D, bool FP8>
@@ -207,6 +387,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         *abort_flag = 0;
         fence_barrier_init();
     }
+    int16_t* heads = reinterpret_cast<int16_t*>(smem + L::kHeads);
+    if (tid < p.h.n_retr + p.h.n_strm) heads[tid] = p.h.head[tid];
+    if (warp == kWarps && lane < 4) tma_prefetch_desc(lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.wk : &maps.wv);
     // Marks of the sequences named once and twice, in the ring before its first tile.
     uint32_t* once = reinterpret_cast<uint32_t*>(smem + L::kRing);
     uint32_t* twice = once + kPagedMaxSeqs / 32;
@@ -214,58 +397,81 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();
-    for (int i = tid; i < p.n; i += kThreads) {
-        const int s = p.seqs[i];
-        const bool in = s >= 0 && s < v.max_seqs;
-        int len = in ? v.seq_len[s] : -1;
-        if (in) {
+    // The entries, four in a row per thread: lengths, then the units before each by a
+    // scan over the CTA. Entries named twice count as skipped.
+    constexpr int kOwn = 4;
+    static_assert(kOwn * kThreads >= kPagedMaxBatch, "every entry has a thread");
+    const int i0 = tid * kOwn;
+    int my_seq[kOwn], my_len[kOwn];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) my_seq[j] = i0 + j < p.n ? p.seqs[i0 + j] : -1;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        if (my_seq[j] >= v.max_seqs) my_seq[j] = -1;
+        my_len[j] = my_seq[j] >= 0 ? v.seq_len[my_seq[j]] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int s = my_seq[j];
+        if (s >= 0) {
             const uint32_t bit = 1u << (s & 31);
             if (atomicOr(&once[s >> 5], bit) & bit) atomicOr(&twice[s >> 5], bit);
-            if (len < 0 || static_cast<int64_t>(len) > static_cast<int64_t>(v.max_pages) * v.P) {
-                if (blockIdx.x == 0) report(v.err, kErrPagedArgument);
-                len = -1;
-            }
         }
-        len_of[i] = len;
-        seq_of[i] = static_cast<uint16_t>(in ? s : 0);
     }
     __syncthreads();
-    if (warp == 0) {  // lengths of entries named twice dropped, tiles counted
-        int sum_r = 0, sum_s = 0;
-        for (int i0 = 0; i0 < p.n; i0 += 32) {
-            const int i = i0 + lane;
-            int len = i < p.n ? len_of[i] : -1;
-            if (len >= 0) {
-                const int s = seq_of[i];
-                if ((twice[s >> 5] >> (s & 31)) & 1u) {
-                    if (blockIdx.x == 0) report(v.err, kErrPagedArgument);
-                    len_of[i] = len = -1;
-                }
-            }
-            const int rows = len > 0 ? len : 0;
-            int r = (rows + kPageTile - 1) / kPageTile;
-            int w = ((rows < v.W ? rows : v.W) + kWinTile - 1) / kWinTile;
-            const int r_own = r, w_own = w;
+    int sum_r = 0, sum_s = 0;
+    bool wrong = false;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(0xffffffffu, r, o), b = __shfl_up_sync(0xffffffffu, w, o);
-                if (lane >= o) {
-                    r += a;
-                    w += b;
-                }
-            }
-            if (i < p.n) {
-                before_r[i] = sum_r + r - r_own;
-                before_s[i] = sum_s + w - w_own;
-            }
-            sum_r += __shfl_sync(0xffffffffu, r, 31);
-            sum_s += __shfl_sync(0xffffffffu, w, 31);
+    for (int j = 0; j < kOwn; ++j) {
+        const int s = my_seq[j];
+        if (s >= 0) {
+            const bool bad = ((twice[s >> 5] >> (s & 31)) & 1u) != 0u || my_len[j] < 0 ||
+                             my_len[j] > v.max_pages << v.P_log2;  // the table holds at most 2^27 tokens
+            wrong |= bad;
+            my_len[j] = bad ? -1 : my_len[j];
         }
-        if (lane == 0) {
-            before_r[p.n] = sum_r;
-            before_s[p.n] = sum_s;
-            fence_proxy_async_smem();  // the marks' words become TMA destinations
+        if (i0 + j < p.n) {
+            before_r[i0 + j] = sum_r;
+            before_s[i0 + j] = sum_s;
+            len_of[i0 + j] = my_len[j];
+            seq_of[i0 + j] = static_cast<uint16_t>(s < 0 ? 0 : s);
         }
+        if (my_len[j] > 0) {  // tiles, and one for the end of the pair
+            sum_r += (my_len[j] + kPageTile - 1) / kPageTile + 1;
+            sum_s += ((my_len[j] < v.W ? my_len[j] : v.W) + kWinTile - 1) / kWinTile + 1;
+        }
+    }
+    if (wrong && blockIdx.x == 0) report(v.err, kErrPagedArgument);
+    __syncwarp();
+    const int own_r = sum_r, own_s = sum_s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum_r, o), y = __shfl_up_sync(0xffffffffu, sum_s, o);
+        sum_r += lane >= o ? x : 0;
+        sum_s += lane >= o ? y : 0;
+    }
+    int2* const of_warp = reinterpret_cast<int2*>(smem + L::kStat);
+    if (lane == 31) of_warp[warp] = make_int2(sum_r, sum_s);
+    fence_proxy_async_smem();  // the marks' words become TMA destinations
+    __syncthreads();
+    int total_r = 0, total_s = 0, off_r = sum_r - own_r, off_s = sum_s - own_s;
+#pragma unroll
+    for (int w = 0; w <= kWarps; ++w) {
+        const int2 x = of_warp[w];
+        off_r += w < warp ? x.x : 0;
+        off_s += w < warp ? x.y : 0;
+        total_r += x.x;
+        total_s += x.y;
+    }
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+        if (i0 + j < p.n) {
+            before_r[i0 + j] += off_r;
+            before_s[i0 + j] += off_s;
+        }
+    if (tid == 0) {
+        before_r[p.n] = total_r;
+        before_s[p.n] = total_s;
     }
     __syncthreads();
     // Rows of empty sequences are zero.
@@ -282,24 +488,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     work.n = p.n;
     work.n_retr = p.h.n_retr;
     work.n_strm = p.h.n_strm;
-    work.of_retr = static_cast<int64_t>(before_r[p.n]) * p.h.n_retr;
-    work.total = work.of_retr + static_cast<int64_t>(before_s[p.n]) * p.h.n_strm;
+    work.of_retr = static_cast<int64_t>(total_r) * p.h.n_retr;
+    const int64_t total = work.of_retr + static_cast<int64_t>(total_s) * p.h.n_strm;
     const int64_t pairs = static_cast<int64_t>(p.n) * (p.h.n_retr + p.h.n_strm);
     int n_cta = gridDim.x;
-    if (n_cta > work.total) n_cta = static_cast<int>(work.total);
+    if (n_cta > total) n_cta = static_cast<int>(total);
     if (n_cta > pairs * kPartsPerPair) n_cta = static_cast<int>(pairs * kPartsPerPair);
     const int c = blockIdx.x;
     if (c >= n_cta) return;
-    const int64_t lo = share_start(work.total, c, n_cta), hi = share_start(work.total, c + 1, n_cta);
+    Segment* const slots = reinterpret_cast<Segment*>(smem + L::kSeg);
 
     if (warp == kWarps) {
         // ------------------------------------------------------------ loads
-        int64_t tile = 0;  // of this CTA
+        work.c = c;
+        work.shares.base = divide(total, n_cta);
+        work.shares.more = static_cast<int>(total - work.shares.base * n_cta);
+        const int64_t lo = work.shares.start(c), hi = work.shares.start(c + 1);
+        int st = 0, round = 0;  // ring position
         int n_seg = 0;
         bool ok = true;
-        for (int64_t u = lo; ok && u < hi; ++n_seg) {
-            const Segment s = work.at(u, hi);
-            const int g = p.h.head[s.idx];
+        Segment s = work.at(lo, hi);
+        for (int64_t u = lo; ok && u < hi;) {
+            if (s.t0 == s.t1) {  // only the end of a pair whose tiles other shares hold
+                u += s.units;
+                if (u < hi) work.next(s, u, hi);
+                continue;
+            }
+            const int g = heads[s.idx];
             const int slot = n_seg & 1;
             if (n_seg >= 2 && !mbar_wait(bar(kQEmpty + slot), ((n_seg >> 1) - 1) & 1, abort_flag)) {
                 ok = false;
@@ -307,24 +522,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             if (lane == 0) {
                 const uint32_t q = base + L::kQ + slot * L::kQSlot;
-                mbar_arrive_expect_tx(bar(kQFull + slot), (p.G + 2) * D * 2);
+                mbar_expect_tx(bar(kQFull + slot), (p.G + 2) * D * 2);
                 bulk_load(q, p.q + s.e * p.q_stride + g * p.G * D, p.G * D * 2, bar(kQFull + slot));
                 bulk_load(q + kMaxG * D * 2, p.k_new + s.e * p.kv_stride + g * D, D * 2, bar(kQFull + slot));
                 bulk_load(q + (kMaxG + 1) * D * 2, p.v_new + s.e * p.kv_stride + g * D, D * 2, bar(kQFull + slot));
             }
             const int rows = s.retr ? s.len : (s.len < v.W ? s.len : v.W);
             const int* row_table = v.table + static_cast<int64_t>(s.seq) * v.max_pages;
-            const int n_pages = (s.len + v.P - 1) / v.P;
+            const int n_pages = (s.len + v.P - 1) >> v.P_log2;
             // Page numbers, 32 at a time: `have` covers [win, win + 32), `next` the 32 behind.
             int win = 0, have = 0, next = 0;
             if (s.retr) {
-                win = static_cast<int>(static_cast<int64_t>(s.t0) * kPageTile / v.P);
+                win = s.t0 * kPageTile >> v.P_log2;  // a sequence has at most 2^27 tokens
                 have = win + lane < n_pages ? row_table[win + lane] : -1;
                 next = win + 32 + lane < n_pages ? row_table[win + 32 + lane] : -1;
             }
-            for (int t = s.t0; t < s.t1; ++t, ++tile) {
-                const int st = static_cast<int>(tile % L::kStages);
-                const int64_t round = tile / L::kStages;
+            // The new token's row goes into the cache here, off the computing warps' path:
+            // lanes 0-15 K, 16-31 V, 16 bytes each. Its loads are issued now and used
+            // behind the segment's tiles.
+            const int new_row = s.new_row = s.retr ? s.len - 1 : window_slot(v, s.len - 1);
+            const int new_tile = new_row / (s.retr ? kPageTile : kWinTile);
+            const int which = lane >> 4, ch = lane & 15;
+            const bool owner = new_tile >= s.t0 && new_tile < s.t1 && ch < D / 8;
+            uint4 fresh = make_uint4(0, 0, 0, 0);
+            int new_page = -1, new_ref = 0;
+            float inv_scale = 1.f;
+            if (owner) {
+                fresh = ld_nc_v4((which ? p.v_new : p.k_new) + s.e * p.kv_stride + g * D + ch * 8);
+                if (s.retr) new_page = row_table[new_row >> v.P_log2];
+                if (FP8) inv_scale = p.kv_scale[g * 4 + 2 + which];
+            }
+            work.find_parts(s, u);  // while the loads above are on their way
+            if (lane == 0) {
+                slots[slot] = s;
+                mbar_arrive(bar(kQFull + slot));  // releases the segment
+            }
+            for (int t = s.t0; t < s.t1; ++t) {
                 if (round > 0 && !mbar_wait(bar(kEmpty + st), (round - 1) & 1, abort_flag)) {
                     ok = false;
                     break;
@@ -334,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     const int row0 = t * kPageTile;
                     const int valid = rows - row0 < kPageTile ? rows - row0 : kPageTile;
                     const int box = v.P < kPageTile ? v.P : kPageTile;  // rows of one copy
-                    const int n_box = (valid + box - 1) / box;
-                    const int pg0 = row0 / v.P;
+                    const int n_box = (valid + box - 1) >> (v.P < kPageTile ? v.P_log2 : kPageTile == 64 ? 6 : 7);
+                    const int pg0 = row0 >> v.P_log2;
                     while (pg0 >= win + 32) {
                         win += 32;
                         have = next;
@@ -359,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     if (mine) {
                         // An unusable page number loads zeros (a coordinate outside the map).
                         const int z = page < 0 ? -1 : page * v.r_all + p.h.r0 + s.idx;
-                        const int y = row0 % v.P;
+                        const int y = row0 & (v.P - 1);
 #pragma unroll
                         for (int cb = 0; cb < kCols; ++cb) {
                             const uint32_t d = dst + cb * (kPageTile * kRowBytes) + lane * box * kRowBytes;
@@ -378,18 +611,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     }
                 }
                 __syncwarp();
+                if (t == s.t0 && new_page >= 0 && new_page < v.num_pages) new_ref = v.ref[new_page];
+                if (++st == L::kStages) {
+                    st = 0;
+                    ++round;
+                }
             }
-            u += s.t1 - s.t0;
+            if (owner) {
+                if (!s.retr) {
+                    bf16* dst = (which ? v.v_window : v.k_window) +
+                                ((static_cast<int64_t>(s.seq) * v.s_all + p.h.s0 + s.idx - p.h.n_retr) * v.W + new_row) * D + ch * 8;
+                    *reinterpret_cast<uint4*>(dst) = fresh;
+                } else if (new_ref > 1) {
+                    report(v.err, kErrPagedShared);
+                } else if (new_page >= 0 && new_page < v.num_pages) {  // else the loads reported it
+                    const int64_t at = ((static_cast<int64_t>(new_page) * v.r_all + p.h.r0 + s.idx) * v.P + (new_row & (v.P - 1))) * D + ch * 8;
+                    uint8_t* pool = which ? v.v_pages : v.k_pages;
+                    if (FP8) *reinterpret_cast<uint2*>(pool + at) = e4m3x8_from_bf16x8(fresh, inv_scale);
+                    else *reinterpret_cast<uint4*>(pool + at * 2) = fresh;
+                }
+            }
+            ++n_seg;
+            u += s.units;
+            if (u < hi) work.next(s, u, hi);
         }
         if (!ok && lane == 0) {
             *abort_flag = 1;
             report(v.err, kErrPagedWait);
         }
+        // The end: a segment without tiles.
+        if (n_seg >= 2) ok = mbar_wait(bar(kQEmpty + (n_seg & 1)), ((n_seg >> 1) - 1) & 1, abort_flag) && ok;
+        if (lane == 0) {
+            slots[n_seg & 1].tiles = 0;
+            mbar_arrive(bar(kQFull + (n_seg & 1)));
+        }
         // Every copy issued lands before the CTA may exit.
-        const int64_t from = tile > L::kStages ? tile - L::kStages : 0;
-        for (int64_t t = from; t < tile; ++t)
-            mbar_wait(bar(kFull + static_cast<int>(t % L::kStages)), (t / L::kStages) & 1, nullptr);
-        for (int i = n_seg > 2 ? n_seg - 2 : 0; i < n_seg; ++i) mbar_wait(bar(kQFull + (i & 1)), (i >> 1) & 1, nullptr);
+        for (int i = 0; i < L::kStages; ++i) {
+            const int rounds = round + (i < st ? 1 : 0);  // times stage i was filled
+            if (rounds > 0) mbar_wait(bar(kFull + i), (rounds - 1) & 1, nullptr);
+        }
+        if (n_seg >= 1) mbar_wait(bar(kQFull + ((n_seg - 1) & 1)), ((n_seg - 1) >> 1) & 1, nullptr);
         return;
     }
 
@@ -397,19 +658,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int gq = lane >> 2;  // row of an accumulator, column of an operand: key / head
     const int cq = lane & 3;
     constexpr int kSteps = D / 16;
-    int64_t tile = 0;
+    int st = 0, round = 0;
     int n_seg = 0;
     bool ok = true;
     float* merge = reinterpret_cast<float*>(smem + L::kMerge);
     float* stat = reinterpret_cast<float*>(smem + L::kStat);  // [warp][head][2]
-    for (int64_t u = lo; u < hi; ++n_seg) {
-        const Segment s = work.at(u, hi);
-        const int g = p.h.head[s.idx];
+    Segment* const pending = slots + 2;
+    int n_pending = 0;
+    for (;; ++n_seg) {
         const int slot = n_seg & 1;
         const uint32_t q = base + L::kQ + slot * L::kQSlot;
         if (ok && !mbar_wait(bar(kQFull + slot), (n_seg >> 1) & 1, abort_flag)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) *abort_flag = 1;
+        const Segment s = slots[slot];
+        if (group_any(!ok) || s.tiles == 0) break;  // the same for all four warps
+        const int g = heads[s.idx];
         const bool codes = FP8 && s.retr;  // operands are f16 made of codes
         // The queries as the B operand: head gq, this thread's part of D.
         uint32_t b[kSteps][2];
@@ -465,12 +729,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         const int rows = s.retr ? s.len : (s.len < v.W ? s.len : v.W);
-        const int new_row = s.retr ? s.len - 1 : window_slot(v, s.len - 1);
+        const int new_row = s.new_row;
         const int tile_rows = s.retr ? kPageTile : kWinTile;
-        for (int t = s.t0; t < s.t1; ++t, ++tile) {
-            const int st = static_cast<int>(tile % L::kStages);
+        for (int t = s.t0; t < s.t1; ++t) {
             const uint32_t kt = base + L::kRing + st * L::kStage, vt = kt + kHalf;
-            if (ok && !mbar_wait(bar(kFull + st), (tile / L::kStages) & 1, abort_flag)) ok = false;
+            if (ok && !mbar_wait(bar(kFull + st), round & 1, abort_flag)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) *abort_flag = 1;
             const int per = tile_rows / kWarps;  // this warp's rows of the tile
@@ -478,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int valid = rows - t * tile_rows - w0;  // of them, rows to attend to
             bool touched = false;
             if (ok && valid > 0) {
-                // The new token's row: into the tile, and into the cache.
+                // The new token's row goes over what the cache held in its place.
                 const int nr = new_row - t * tile_rows - w0;
                 if (nr >= 0 && nr < per) {
                     touched = true;
@@ -494,36 +757,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         } else {
                             sts128((which ? vt : kt) + (ch >> 3) * (tile_rows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), x);
                         }
-                        if (!s.retr) {
-                            bf16* dst = (which ? v.v_window : v.k_window) +
-                                        ((static_cast<int64_t>(s.seq) * v.s_all + p.h.s0 + s.idx - p.h.n_retr) * v.W + new_row) * D + ch * 8;
-                            *reinterpret_cast<uint4*>(dst) = x;
-                        } else {
-                            const int page = v.table[static_cast<int64_t>(s.seq) * v.max_pages + new_row / v.P];
-                            const bool in = page >= 0 && page < v.num_pages;  // else the loads reported it
-                            if (in && v.ref[page] > 1) {
-                                report(v.err, kErrPagedShared);
-                            } else if (in) {
-                                const int64_t at = ((static_cast<int64_t>(page) * v.r_all + p.h.r0 + s.idx) * v.P + new_row % v.P) * D + ch * 8;
-                                uint8_t* pool = which ? v.v_pages : v.k_pages;
-                                if (FP8) *reinterpret_cast<uint2*>(pool + at) = e4m3x8_from_bf16x8(x, p.kv_scale[g * 4 + 2 + which]);
-                                else *reinterpret_cast<uint4*>(pool + at * 2) = x;
-                            }
-                        }
                     }
                 }
                 if (valid < per) {  // V rows behind the last one
                     touched = true;
-                    for (int r = w0 + valid; r < w0 + per; ++r) {
-                        if (codes) {
-                            if (lane < D / 16) sts128(vt + r * D + lane * 16, make_uint4(0, 0, 0, 0));
-                        } else if (lane < D / 8) {
-                            sts128(vt + (lane >> 3) * (tile_rows * 128) + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+                    constexpr int kPieces = D / 8;  // 16 bytes each of a bf16 row; half as many of codes
+                    if (codes) {
+                        for (int i = lane; i < (per - valid) * (kPieces / 2); i += 32)
+                            sts128(vt + (w0 + valid) * D + i * 16, make_uint4(0, 0, 0, 0));
+                    } else {
+                        for (int i = lane; i < (per - valid) * kPieces; i += 32) {
+                            const int r = w0 + valid + i / kPieces, ch = i % kPieces;
+                            sts128(vt + (ch >> 3) * (tile_rows * 128) + r * 128 + (ch & 7) * 16, make_uint4(0, 0, 0, 0));
                         }
                     }
                 }
                 __syncwarp();
                 const int parts = per / 16;  // 1, or 2 with codes
+#pragma unroll 1
                 for (int part = 0; part < parts; ++part) {
                     const int r0 = w0 + part * 16;
                     const int left = valid - part * 16;
@@ -641,6 +892,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (touched) fence_proxy_async_smem();  // before TMA writes the stage again
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kEmpty + st));
+            if (++st == L::kStages) {
+                st = 0;
+                ++round;
+            }
         }
         if (lane == 0) mbar_arrive(bar(kQEmpty + slot));
         // ------------------------------------------------------------ end of the segment
@@ -684,100 +939,90 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             o[i][2] *= f[0];
             o[i][3] *= f[1];
         }
-        // Row of D that accumulator i holds in its first (half 0) or second pair.
+        // O: warp w ends up with the sums of quarter w of the accumulators.
+        float r[kSteps / kWarps][4];
+        if (warp == 0) gather_quarter<0, kSteps>(o, r, merge, lane);
+        else if (warp == 1) gather_quarter<1, kSteps>(o, r, merge, lane);
+        else if (warp == 2) gather_quarter<2, kSteps>(o, r, merge, lane);
+        else gather_quarter<3, kSteps>(o, r, merge, lane);
+        const int i0 = warp * (kSteps / kWarps);
+        // Column of D that accumulator i holds in its first (half 0) or second pair.
         auto col = [&](int i, int half) { return codes ? gq * (D / 8) + 2 * i + half : i * 16 + half * 8 + gq; };
-        for (int w = 1; w < kWarps; ++w) {
-            if (warp == w) {
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (2 * cq + (j & 1) < p.G) merge[(i * 4 + j) * 32 + lane] = o[i][j];
-            }
-            group_sync();
-            if (warp == 0) {
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (2 * cq + (j & 1) < p.G) o[i][j] += merge[(i * 4 + j) * 32 + lane];
-            }
-            group_sync();
-        }
         const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-        const float v_scale = codes ? p.kv_scale[g * 4 + 1] : 1.f;
         if (whole) {
-            if (warp == 0 && ok) {
+            const float v_scale = codes ? p.kv_scale[g * 4 + 1] : 1.f;
+            const float inv[2] = {v_scale / lj[0], v_scale / lj[1]};
+            bf16* dst = p.out + s.e * p.out_stride + (g * p.G + 2 * cq) * D;
+            if (ok) {
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i)
+                for (int h = 0; h < 2; ++h)
+                    if (2 * cq + h < p.G)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int h = 2 * cq + (j & 1);
-                        if (h < p.G)
-                            p.out[s.e * p.out_stride + (g * p.G + h) * D + col(i, j >> 1)] =
-                                __float2bfloat16(o[i][j] * (v_scale / lj[j & 1]));
-                    }
+                        for (int i = 0; i < kSteps / kWarps; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                dst[h * D + col(i0 + i, j)] = __float2bfloat16(r[i][2 * j + h] * inv[h]);
             }
         } else {
-            const int part = c * 2 + (u == lo ? 0 : 1);
-            if (warp == 0) {
-                float* po = p.part_o + static_cast<int64_t>(part) * p.G * D;
-                float* pm = p.part_ml + static_cast<int64_t>(part) * p.G * 2;
+            const int part = 2 * c + (s.t0 == 0 && s.part0 == 2 * c + 1 ? 1 : 0);
+            float* po = p.part_o + (static_cast<int64_t>(part) * p.G + 2 * cq) * D;
+            float* pm = p.part_ml + static_cast<int64_t>(part) * p.G * 2;
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i)
+            for (int h = 0; h < 2; ++h)
+                if (2 * cq + h < p.G)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int h = 2 * cq + (j & 1);
-                        if (h < p.G) po[h * D + col(i, j >> 1)] = o[i][j];
+                    for (int i = 0; i < kSteps / kWarps; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) po[h * D + col(i0 + i, j)] = r[i][2 * j + h];
+            if (warp == 0 && gq == 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (2 * cq + i < p.G) {
+                        pm[(2 * cq + i) * 2] = mj[i];
+                        pm[(2 * cq + i) * 2 + 1] = lj[i];
                     }
-                if (gq == 0) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (2 * cq + i < p.G) {
-                            pm[(2 * cq + i) * 2] = mj[i];
-                            pm[(2 * cq + i) * 2 + 1] = lj[i];
-                        }
-                }
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) {
-                    const int c0 = share_of(work.total, s.first, n_cta);
-                    const int c1 = share_of(work.total, s.first + s.tiles - 1, n_cta);
-                    uint32_t* counter = p.counters + s.e * p.Hkv + s.idx;
-                    const uint32_t done = atomicAdd(counter, 1u);
-                    const bool last = done == static_cast<uint32_t>(c1 - c0);
-                    if (last) *counter = 0u;  // for the next launch
-                    *last_flag = last ? 1u : 0u;
-                }
             }
-            group_sync();
-            const bool last = *last_flag != 0u;
-            group_sync();
-            if (last) {
-                __threadfence();
-                const int c0 = share_of(work.total, s.first, n_cta);
-                const int c1 = share_of(work.total, s.first + s.tiles - 1, n_cta);
-                // Part of CTA k: its first segment unless the pair starts inside its share.
-                auto part_of = [&](int k) { return k * 2 + (s.first <= share_start(work.total, k, n_cta) ? 0 : 1); };
-                for (int i = tid; i < p.G * D; i += kWarps * 32) {
-                    const int h = i / D;
-                    float m = -INFINITY;
-                    for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg(p.part_ml + (static_cast<int64_t>(part_of(k)) * p.G + h) * 2));
-                    float sum = 0.f, acc = 0.f;
-                    for (int k = c0; k <= c1; ++k) {
-                        const int64_t a = static_cast<int64_t>(part_of(k)) * p.G + h;
-                        const float mk = __ldcg(p.part_ml + a * 2), lk = __ldcg(p.part_ml + a * 2 + 1);
-                        const float w = mk == m ? 1.f : fast_exp2(mk - m);
-                        sum += lk * w;
-                        acc += __ldcg(p.part_o + a * D + i % D) * w;
-                    }
-                    p.out[s.e * p.out_stride + g * p.G * D + i] = __float2bfloat16(acc * (v_scale / sum));
-                }
-            }
+            if (tid == 0) pending[n_pending] = s;
+            ++n_pending;
         }
-        u += s.t1 - s.t0;
+        // The next segment's group_any() is the barrier behind the last reads of stat and merge.
     }
     if (!ok && lane == 0) report(v.err, kErrPagedWait);
+    // ---------------------------------------------------------------- cut pairs
+    // A share cuts at most two pairs, at its ends. They are counted here, behind all
+    // tiles: each step of the chain (writes out, count, other parts in) takes a
+    // memory latency, which is several times longer while the tiles stream.
+    if (n_pending > 0) {
+        group_sync();
+        if (tid == 0) {
+            // Releases the CTA's writes (ordered before by the barrier), then acquires
+            // the other parts' of the pairs that it is the last to finish.
+            asm volatile("fence.acq_rel.gpu;" ::: "memory");
+            uint32_t* const c0 = p.counters + pending[0].e * p.Hkv + pending[0].idx;
+            uint32_t* const c1 = p.counters + pending[1].e * p.Hkv + pending[1].idx;
+            const uint32_t b0 = atomicAdd(c0, 1u);
+            const uint32_t b1 = n_pending > 1 ? atomicAdd(c1, 1u) : 0u;
+            uint32_t last = 0;
+            if (b0 + 1u == static_cast<uint32_t>(pending[0].parts)) {
+                last |= 1u;
+                *c0 = 0u;  // for the next launch
+            }
+            if (n_pending > 1 && b1 + 1u == static_cast<uint32_t>(pending[1].parts)) {
+                last |= 2u;
+                *c1 = 0u;
+            }
+            asm volatile("fence.acq_rel.gpu;" ::: "memory");
+            *last_flag = ok ? last : 0u;
+        }
+        group_sync();
+        for (int i = 0; i < n_pending; ++i)
+            if ((*last_flag >> i) & 1u) {
+                const Segment s = pending[i];
+                const int g = heads[s.idx];
+                join_parts<D>(p, s, g, FP8 && s.retr ? p.kv_scale[g * 4 + 1] : 1.f, merge, warp, lane);
+                group_sync();  // the joining buffer is free again
+            }
+    }
 }
 
 template <int D, bool FP8>

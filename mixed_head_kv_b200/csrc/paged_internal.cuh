@@ -34,6 +34,7 @@ struct PagedView {
     int32_t max_seqs, max_pages, num_pages, P, D, S, R, W;  // S, R: sink and recent; W = S + R
     int32_t r_all, s_all;  // retrieval / streaming heads of all layers
     int32_t elem;          // bytes per element of the pages
+    int32_t P_log2;        // P is a power of two
 };
 
 // KV heads of one layer: retrieval heads first, then streaming heads, each with

@@ -197,6 +197,38 @@ def test_decode_long_sequences_are_split_and_joined(duo, fp8):
     assert c.error_flags() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,G,Hkv", [(512, 1, 8), (300, 8, 2), (33, 4, 16)])
+def test_decode_many_entries(duo, n, G, Hkv, fp8):
+    """Every CTA works through several pairs: the largest batch, short and empty sequences among them."""
+    c = make(duo, Hkv=Hkv, G=G, D=64, P=16, S=4, R=60, num_pages=n * 12, max_pages=40, max_seqs=n + 5, fp8=fp8)
+    sc = scales_for(c) if fp8 else None
+    if fp8:
+        c.set_kv_scales(0, *sc)
+    rng = random.Random(n)
+    model, rows = Model(n * 12, 16, 40, n + 5), Rows(c)
+    fill(c, model, rows, [rng.choice([0, 1, 15, 16, 40, 64, 130, 300]) for _ in range(n)], seed=2)
+    order = list(range(n))
+    rng.shuffle(order)
+    assert model.extend(order, [1] * n)
+    c.extend(ints(order))
+    q, k, v = (normal(n, h, 64, seed=h) for h in (Hkv * G, Hkv, Hkv))
+    out = torch.full_like(q, float("nan"))
+    t0 = torch.cuda.Event(enable_timing=True)
+    t1 = torch.cuda.Event(enable_timing=True)
+    c.decode(0, ints(order), q, k, v, out)
+    t0.record()
+    c.decode(0, ints(order), q, k, v, out)
+    t1.record()
+    for i, s in enumerate(order):
+        rows.add(s, k[None, i:i + 1], v[None, i:i + 1])
+        if i % 7 == 0:
+            ref, w = rows.attention(0, s, q[i:i + 1], [model.len[s] - 1], 1 / 8, sc)
+            check_out(out[i:i + 1], ref, w, f"entry {i}")
+    assert torch.isfinite(out).all() and c.error_flags() == 0
+    assert t0.elapsed_time(t1) < 200  # no bounded wait (1 s) ran out
+
+
 def test_decode_offsets_past_32_bits(duo):
     """A pool of more than 2^32 bytes in one tensor: the last pages are read and written where they are."""
     num_pages = 20000

@@ -96,7 +96,7 @@ class _Fake(duo.PagedCache):
         self.layout = layout()
         self.device = torch.device("cpu")
         self.handle = None
-        self._int32, self._bf16 = torch.int32, torch.bfloat16
+        self._constants()
 
 
 def test_tensor_checks():

@@ -33,6 +33,8 @@
 // more than 2^8 (exact), sums in 32 bits; P rounded to bf16, the operand type
 // (relative 2^-9 per term). Every mbarrier wait is bounded; on timeout the CTA
 // records kErrPagedWait and unwinds.
+#include <type_traits>
+
 #include "paged_internal.cuh"
 #include "prefill_common.cuh"
 
@@ -154,6 +156,41 @@ __device__ __forceinline__ void give_up(uint32_t* err, volatile int* abort_flag)
     atomicOr(err, kErrPagedWait);
 }
 
+// 1 in one lane of the warp, the same in every call.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// The products and commits of sm100.cuh, issued by the lanes with `lead` set only.
+__device__ __forceinline__ void tc_mma_ss_by(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts_by(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_by(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
+        : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -263,27 +300,31 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         regs_dec<kOtherRegs>();
         if (warp == 8 && lane == 0) {
             // -------------------------------------------------------- items, Q and K
+            // The next item is taken and published before this one's K tiles are loaded,
+            // so that nobody waits for the counter.
             tma_prefetch_desc(&maps.q);
-            int g = 0;  // K tiles issued
-            int q_loads = 0;
-            for (int ord = 0;; ++ord) {
-                const unsigned i = atomicAdd(p.work, 1u);
-                const bool more = i < n_items && *abort_flag == 0;
-                PackItem it;
+            int published = 0;
+            auto publish = [&](PackItem& it) -> bool {
+                const unsigned i = *abort_flag == 0 ? atomicAdd(p.work, 1u) : 0xFFFFFFFFu;
                 it.idx = -1;
-                if (more) it = pack_item(p, prompts, i);
-                const int slot = ord % kQueueSlots;
-                if (ord >= kQueueSlots && !mbar_wait(bar(kItemEmpty + slot), ((ord / kQueueSlots) - 1) & 1, abort_flag)) {
-                    give_up(p.err, abort_flag);
-                    break;
-                }
+                if (i < n_items) it = pack_item(p, prompts, i);
+                const int slot = published % kQueueSlots;
+                if (published >= kQueueSlots &&
+                    !mbar_wait(bar(kItemEmpty + slot), ((published / kQueueSlots) - 1) & 1, abort_flag))
+                    return false;
                 queue[slot] = it;
                 mbar_arrive(bar(kItemFull + slot));
-                if (!more) break;
-                if (ord >= 1 && !mbar_wait(bar(kQEmpty), (ord - 1) & 1, abort_flag)) {
-                    give_up(p.err, abort_flag);
-                    break;
-                }
+                ++published;
+                return true;
+            };
+            int g = 0;  // K tiles issued
+            int q_loads = 0;
+            PackItem it, after;
+            bool ok = publish(it);
+            while (ok && it.idx >= 0) {
+                ok = publish(after);
+                if (ok && q_loads >= 1) ok = mbar_wait(bar(kQEmpty), (q_loads - 1) & 1, abort_flag);
+                if (!ok) break;
                 mbar_arrive_expect_tx(bar(kQFull), (it.nb > 0 ? 2 : 1) * Lay::kTile);
                 for (int kb = 0; kb < Lay::kColBlocks; ++kb) {
                     tma_load_3d(sQ + kb * kTileBytesPerColBlock, &maps.q, bar(kQFull), kb * 64, it.head_a, it.start + it.qa);
@@ -291,9 +332,8 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                         tma_load_3d(sQ + Lay::kTile + kb * kTileBytesPerColBlock, &maps.q, bar(kQFull), kb * 64, it.head_b,
                                     it.start + it.qb);
                 }
-                q_loads = ord + 1;
+                ++q_loads;
                 const int n = it.na > it.nb ? it.na : it.nb;
-                bool ok = true;
                 for (int j = 0; j < n; ++j, ++g) {
                     const int st = g & 1;
                     if (g >= 2 && !mbar_wait(bar(kKEmpty + st), ((g >> 1) - 1) & 1, abort_flag)) {
@@ -305,11 +345,9 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                         tma_load_3d(sK + st * Lay::kTile + kb * kTileBytesPerColBlock, &maps.k, bar(kKFull + st), kb * 64,
                                     it.g, it.start + key_row(it, j));
                 }
-                if (!ok) {
-                    give_up(p.err, abort_flag);
-                    break;
-                }
+                it = after;
             }
+            if (!ok) give_up(p.err, abort_flag);
             // Every load issued lands before the CTA may exit.
             for (int j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_wait(bar(kKFull + (j & 1)), (j >> 1) & 1, nullptr);
             if (q_loads > 0) mbar_wait(bar(kQFull), (q_loads - 1) & 1, nullptr);
@@ -360,83 +398,95 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 }
             }
             for (int j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_wait(bar(kVFull + (j & 1)), (j >> 1) & 1, abort_flag);
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == 9) {
             // -------------------------------------------------------- products
+            // The whole warp walks the loop and one elected lane issues: control flow and
+            // descriptors stay uniform over the warp. One lane on its own took 4100 cycles
+            // per pair of tiles to issue what the tensor core computes in 2048.
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kTileK, 0, 0);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+            const uint32_t lead = elect_lane();
+            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
+            const uint64_t dv = smem_desc_sw128(sV, kTileBytesPerColBlock, 1024);
             int g = 0;               // K/V tiles of the items before
-            int count[2] = {0, 0};   // products PV of each tile so far
-            int items[2] = {0, 0};   // items that had the tile so far
+            int count_a = 0, count_b = 0;  // products PV of each tile so far
+            int items_a = 0, items_b = 0;  // items that had the tile so far
             bool ok = true;
             for (int ord = 0; ok; ++ord) {
                 PackItem it;
                 const bool more = take_item(ord, it);
-                free_item(ord);
-                if (!more) break;
-                const int nt[2] = {it.na, it.nb};
-                const int n = it.na > it.nb ? it.na : it.nb;
-                ok = mbar_wait(bar(kQFull), ord & 1, abort_flag);
-                int k_ready = 0, v_ready = 0;
-                // S(x) = Q(x) K(j)^T
-                auto qk = [&](int x, int j) {
+                __syncwarp();
+                if (lead) free_item(ord);
+                if (!__all_sync(0xffffffffu, more)) break;
+                const int na = __shfl_sync(0xffffffffu, it.na, 0), nb = __shfl_sync(0xffffffffu, it.nb, 0);
+                const int n = na > nb ? na : nb;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFull), ord & 1, abort_flag));
+                // S(x) = Q(x) K(j)^T; `last`: the last to read the K tile.
+                auto qk = [&](auto x_, int j, bool wait, bool last) {
+                    constexpr int x = decltype(x_)::value;
                     const int st = (g + j) & 1;
-                    if (k_ready <= j) {
-                        if (!mbar_wait(bar(kKFull + st), ((g + j) >> 1) & 1, abort_flag)) return false;
-                        k_ready = j + 1;
-                    }
+                    if (wait && !__all_sync(0xffffffffu, mbar_wait(bar(kKFull + st), ((g + j) >> 1) & 1, abort_flag))) return false;
                     tc_fence_after();
-                    const uint32_t q = sQ + x * Lay::kTile, k = sK + st * Lay::kTile;
+                    const uint64_t q = dq + x * (Lay::kTile >> 4), k = dk + st * (Lay::kTile >> 4);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kTileBytesPerColBlock + (kk & 3) * 32;
-                        tc_mma_ss(tmem + x * kTileK, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024),
-                                  idesc_qk, kk > 0 ? 1u : 0u);
+                        const uint32_t off = ((kk >> 2) * kTileBytesPerColBlock + (kk & 3) * 32) >> 4;
+                        tc_mma_ss_by(lead, tmem + x * kTileK, q + off, k + off, idesc_qk, kk > 0 ? 1u : 0u);
                     }
-                    tc_commit(bar(kSFull + x));
-                    if (x == 1 || j >= nt[1]) {  // the last to read the tile
-                        tc_commit(bar(kKEmpty + st));
-                        if (j + 1 == n) tc_commit(bar(kQEmpty));
+                    tc_commit_by(lead, bar(kSFull + x));
+                    if (last) {
+                        tc_commit_by(lead, bar(kKEmpty + st));
+                        if (j + 1 == n) tc_commit_by(lead, bar(kQEmpty));
                     }
                     return true;
                 };
-                // O(x) += P(x) V(j)
-                auto pv = [&](int x, int j) {
+                // O(x) += P(x) V(j); `last`: the last to read the V tile.
+                auto pv = [&](auto x_, int j, bool wait, bool last, int count, int items) {
+                    constexpr int x = decltype(x_)::value;
                     const int st = (g + j) & 1;
-                    if (v_ready <= j) {
-                        if (!mbar_wait(bar(kVFull + st), ((g + j) >> 1) & 1, abort_flag)) return false;
-                        v_ready = j + 1;
-                    }
-                    if (j == 0 && items[x] > 0 && !mbar_wait(bar(kOEmpty + x), (items[x] - 1) & 1, abort_flag)) return false;
-                    const uint32_t vt = sV + st * Lay::kTile;
+                    if (wait && !__all_sync(0xffffffffu, mbar_wait(bar(kVFull + st), ((g + j) >> 1) & 1, abort_flag))) return false;
+                    if (j == 0 && items > 0 &&
+                        !__all_sync(0xffffffffu, mbar_wait(bar(kOEmpty + x), (items - 1) & 1, abort_flag)))
+                        return false;
+                    const uint64_t vt = dv + st * (Lay::kTile >> 4);
+#pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        if (!mbar_wait(bar(kPFull + 2 * x + half), count[x] & 1, abort_flag)) return false;
+                        if (!__all_sync(0xffffffffu, mbar_wait(bar(kPFull + 2 * x + half), count & 1, abort_flag))) return false;
                         tc_fence_after();
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4) {
                             const int kk = half * 4 + k4;
-                            tc_mma_ts(tmem + kTmemO + x * 128, tmem + x * kTileK + kk * 8,
-                                      smem_desc_sw128(vt + kk * 2048, kTileBytesPerColBlock, 1024), idesc_pv,
-                                      (j > 0 || kk > 0) ? 1u : 0u);
+                            tc_mma_ts_by(lead, tmem + kTmemO + x * 128, tmem + x * kTileK + kk * 8, vt + kk * (2048 >> 4),
+                                         idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
                         }
                     }
-                    tc_commit(bar(kODone + x));
-                    if (x == 1 || j >= nt[1]) tc_commit(bar(kVEmpty + st));
-                    ++count[x];
+                    tc_commit_by(lead, bar(kODone + x));
+                    if (last) tc_commit_by(lead, bar(kVEmpty + st));
                     return true;
                 };
-                for (int x = 0; ok && x < 2; ++x)
-                    if (nt[x] > 0) ok = qk(x, 0);
-                for (int j = 0; ok && j < n; ++j)
-                    for (int x = 0; ok && x < 2; ++x) {
-                        if (j >= nt[x]) continue;
-                        ok = pv(x, j);
-                        if (ok && j + 1 < nt[x]) ok = qk(x, j + 1);
+                constexpr std::integral_constant<int, 0> A{};
+                constexpr std::integral_constant<int, 1> B{};
+                // The tiles' lists differ by one tile at most, or one is empty.
+                if (ok && na > 0) ok = qk(A, 0, true, nb == 0);
+                if (ok && nb > 0) ok = qk(B, 0, na == 0, true);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j < na) {
+                        ok = pv(A, j, true, j >= nb, count_a, items_a);
+                        ++count_a;
+                        if (ok && j + 1 < na) ok = qk(A, j + 1, true, j + 1 >= nb);
                     }
-                for (int x = 0; x < 2; ++x) items[x] += nt[x] > 0;
+                    if (ok && j < nb) {
+                        ok = pv(B, j, j >= na, true, count_b, items_b);
+                        ++count_b;
+                        if (ok && j + 1 < nb) ok = qk(B, j + 1, j + 1 >= na, true);
+                    }
+                }
+                items_a += na > 0;
+                items_b += nb > 0;
                 g += n;
             }
-            if (!ok) give_up(p.err, abort_flag);
-            tc_commit(bar(kDrain));  // every product issued has completed before TMEM is released
+            if (!ok && lead) give_up(p.err, abort_flag);
+            tc_commit_by(lead, bar(kDrain));  // every product issued has completed before TMEM is released
             mbar_wait(bar(kDrain), 0, nullptr);
         }
         __syncwarp();
@@ -520,24 +570,23 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 const uint64_t negm = f2pack(-m_use, -m_use);
                 uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
+                    for (int i = 0; i < 32; i += 2) {
                         float e0, e1;
-                        f2unpack(ffma2(f2pack(__uint_as_float(s[2 * h + (i >> 5)][i & 31]),
-                                              __uint_as_float(s[2 * h + (i >> 5)][(i & 31) + 1])),
-                                       scale2, negm),
-                                 e0, e1);
+                        f2unpack(ffma2(f2pack(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), scale2, negm), e0, e1);
                         const float p0 = fast_exp2(e0), p1 = fast_exp2(e1);
                         acc[(i >> 1) & 1] = fadd2(acc[(i >> 1) & 1], f2pack(p0, p1));
                         pk[i >> 1] = pack_bf16x2(p0, p1);
                     }
-                    tmem_st32(tS + h * 32, pk);  // every S column has been read
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kPFull + 2 * x + h));
+                    tmem_st16(tS + c * 16, pk);  // every S column has been read
+                    if (c & 1) {
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kPFull + 2 * x + (c >> 1)));
+                    }
                 }
                 float a0, a1;
                 f2unpack(fadd2(acc[0], acc[1]), a0, a1);

@@ -461,9 +461,8 @@ DUO_API duo_status duo_paged_append(duo_paged* cache, int32_t layer, int32_t n, 
  * itself in retrieval heads, sinks and window in streaming heads). Rows of
  * another prompt or outside every range have no effect on it, whatever they
  * hold, and out rows outside every range are not written. An empty prompt is
- * allowed. Within a prompt a NaN or infinite v row also reaches the queries
- * before it in the same 128-token tile. Neither reads nor changes the cache
- * (duo_paged_append stores the rows). n_rows: rows of the tensors, below 2^30;
+ * allowed. Neither reads nor changes the cache (duo_paged_append stores the
+ * rows). n_rows: rows of the tensors, below 2^30;
  * an entry whose range is not within [0, n_rows] or runs backwards is skipped
  * (DUO_ERR_BIT_PAGED_ARGUMENT). */
 DUO_API duo_status duo_paged_prefill(duo_paged* cache, int32_t layer, int32_t n, const int32_t* row_start,

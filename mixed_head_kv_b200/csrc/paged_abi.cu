@@ -363,6 +363,8 @@ duo_status duo_paged_prefill(duo_paged* c, int32_t layer, int32_t n, const int32
         return DUO_ERR_CUDA;
     PackedPrefillParams p{};
     p.out = static_cast<bf16*>(out);
+    p.v = static_cast<const bf16*>(v);
+    p.kv_stride = ks;
     p.row_start = row_start;
     p.err = c->view.err;
     p.work = c->work;

@@ -116,6 +116,8 @@ cudaError_t launch_paged_decode(const PagedDecodeParams& p, const PagedMaps& m, 
 // ------------------------------------------------------------------ packed prompts
 struct PackedPrefillParams {
     bf16* out;
+    const bf16* v;
+    int64_t kv_stride;
     const int32_t* row_start;
     uint32_t* err;
     uint32_t* work;  // [0] next work item, [1] CTAs done; zero between launches

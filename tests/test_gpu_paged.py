@@ -394,6 +394,62 @@ def test_prefill_poisoned_neighbour_and_large_scores(duo):
     check_prompts(c, 0, [0, start[1]], q, k, v64, out)
 
 
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("S,R", [(4, 40), (130, 300)])
+def test_prefill_non_finite_values_reach_their_readers_only(duo, G, S, R):
+    """Infinite and NaN value rows: exactly the queries that see such a row get them, in its columns alone."""
+    lens = [500, 20, 3, 60, 0, 9, 700]  # the short ones share tiles
+    c = make(duo, Hkv=2, G=G, D=128, S=S, R=R)
+    start, (q, k, v) = packed(lens, 2 * G, 2, 128, seed=S)
+    inf, nan = float("inf"), float("nan")
+    odd = torch.zeros(v.shape, dtype=torch.float64, device="cuda")
+    for row, col, x in ((5, 3, inf), (120, 7, -inf), (130, 3, nan), (400, 64, inf), (499, 1, nan), (505, 9, inf), (521, 100, -inf),
+                        (540, 11, nan), (585, 127, inf), (592, 0, nan), (600, 5, -inf), (900, 5, inf), (1291, 8, nan)):
+        odd[row, :, col] = x
+    bad = ~torch.isfinite(odd)
+    clean = v.clone()
+    clean[bad] = 0
+    v[bad] = odd[bad].to(v.dtype)
+    out = torch.full_like(q, 7.0)
+    c.prefill(0, ints(start), q, k, v, out)
+    from paged_harness import attend
+    for a, b in zip(start, start[1:]):
+        i = torch.arange(b - a, device="cuda")
+        for h in range(2):
+            ref, w = attend(q[a:b, h * G:h * G + G], k[a:b, h], clean[a:b, h], i, S, R, h == 0, 1 / math.sqrt(128))
+            seen = i[None] <= i[:, None]
+            if h == 1:
+                seen &= (i[None] < S) | (i[:, None] - i[None] < R)
+            extra = torch.zeros((b - a, 128), dtype=torch.float64, device="cuda")
+            for j in range(b - a):
+                if bad[a + j, h].any():
+                    extra = extra + torch.where(seen[:, j, None] & bad[a + j, h], odd[a + j, h], 0.0)
+            got, special = out[a:b, h * G:h * G + G].double(), ~torch.isfinite(extra)
+            special = special[:, None].expand(-1, G, -1)
+            want = extra[:, None].expand(-1, G, -1)
+            assert torch.equal(torch.isnan(got), torch.isnan(want)), (a, h)
+            assert torch.equal(torch.isinf(got), torch.isinf(want)) and torch.equal(got[torch.isinf(got)], want[torch.isinf(want)])
+            keep = ~special
+            check_out(got[keep], ref[keep], w[keep], f"prompt at {a}, head {h}")
+    assert c.error_flags() == 0
+
+
+@pytest.mark.parametrize("S,R", [(4, 5), (0, 300), (40, 16)])
+@pytest.mark.parametrize("G", [1, 4])
+def test_prefill_prompts_that_share_tiles(duo, G, S, R):
+    """Runs of short prompts between long ones, an unusable range among them: every row of every prompt."""
+    c = make(duo, Hkv=2, G=G, D=64, S=S, R=R)
+    lens = [30, 1, 96, 1, 128, 127, 2, 200, 0, 0, 64, 64, 64, 1, 1, 1, 1, 300, 5]
+    start, (q, k, v) = packed(lens, 2 * G, 2, 64, seed=R, tail=40)
+    out = torch.full_like(q, 7.0)
+    rs = start + [start[-1] - 3, start[-1] + 20, start[-1] + 37]  # backwards; then two prompts over the last rows
+    c.prefill(0, ints(rs), q, k, v, out)
+    assert c.error_flags() == duo.DUO_ERR_BIT_PAGED_ARGUMENT
+    check_prompts(c, 0, start[:-1], q, k, v, out)  # (the last prompt's final rows are the next but one's too)
+    check_prompts(c, 0, [start[-1] + 20, start[-1] + 37], q, k, v, out)
+    assert (out[start[-1] + 37:] == 7).all()
+
+
 def test_prefill_many_prompts_strided(duo):
     """More prompts than SMs, out of a fused projection, into a wider tensor."""
     c = make(duo, Hkv=2, G=2, D=64, S=4, R=16)

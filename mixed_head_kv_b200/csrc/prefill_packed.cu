@@ -22,10 +22,10 @@
 //
 // Warp roles (384 threads; registers moved from the last group to the others):
 //   warps 0-3  softmax of tile A, one thread per row    warps 4-7  of tile B
-//   warp 8     takes the items, loads Q and the K tiles (2 stages)
+//   warp 8     takes the items, loads Q, the K and the V tiles (2 stages each)
 //   warp 9     issues the products (one thread), owns TMEM
-//   warp 10    loads the V tiles (2 stages); warps 10 and 11 clear the tiles that
-//              are seen in part of what a weight of zero must not meet
+//   warps 10-11 clear the V tiles that are seen in part of what a weight of zero
+//              must not meet
 // TMEM (512 columns): S of A and B, 128 columns each, P (bf16) written over the S
 // it was made from, O of A and of B at 256.
 // Softmax in the exp2 domain; the running maximum moves only when it grows by
@@ -109,29 +109,34 @@ constexpr int kDrain = 29;
 constexpr int kQueueSlots = 4;
 constexpr int kConsumers = 11;  // 8 softmax warps, the issuer, 2 V warps
 
+// Whether some row of the item's tiles sees a part only of the key tile from row0.
+__device__ __forceinline__ bool seen_in_part(const PackedPrefillParams& p, const PackItem& it, int row0) {
+    const int last_row = (it.nb > 0 ? it.qb : it.qa) + kTileQ - 1;
+    return row0 + kTileK > it.qa || (!it.retr && row0 + kTileK > p.S && row0 <= last_row - p.R);
+}
+
 // Query tiles of a prompt of `len` rows.
 __device__ __forceinline__ int query_tiles(int len, int rows) { return (len + rows - 1) / rows; }
 
-__device__ __forceinline__ PackItem pack_item(const PackedPrefillParams& p, const Prompts& pr, int64_t idx) {
+// One copy, as it is long and two places need it. Item numbers fit 32 bits: at most
+// 2^23 + 512 query tiles of 256 heads.
+__device__ __noinline__ PackItem pack_item(const PackedPrefillParams& p, const Prompts& pr, uint32_t idx) {
     PackItem it;
     const bool by_heads = (p.G & 1) == 0;       // tile pair = two heads of a group, or 256 rows of one
     const int rows = by_heads ? kTileQ : 2 * kTileQ;
-    const int per_kv = by_heads ? p.G / 2 : p.G;
-    const int64_t n_tiles = pr.tiles_before[pr.n_groups];
-    const int64_t of_retr = n_tiles * p.h.n_retr * per_kv;
+    const uint32_t per_kv = by_heads ? p.G / 2 : p.G;
+    const uint32_t of_retr = pr.tiles_before[pr.n_groups] * p.h.n_retr * per_kv;
     it.retr = idx < of_retr;
-    const int units = (it.retr ? p.h.n_retr : p.h.n_strm) * per_kv;
-    const int64_t x = it.retr ? idx : idx - of_retr;
+    const uint32_t units = (it.retr ? p.h.n_retr : p.h.n_strm) * per_kv;
+    const uint32_t x = it.retr ? idx : idx - of_retr;
+    const uint32_t tile = x / units, unit = x - tile * units;
     int lo = 0, up = pr.n_groups - 1;
     while (lo < up) {
         const int mid = (lo + up + 1) >> 1;
-        if (static_cast<int64_t>(pr.tiles_before[mid]) * units <= x) lo = mid;
+        if (static_cast<uint32_t>(pr.tiles_before[mid]) <= tile) lo = mid;
         else up = mid - 1;
     }
-    const int64_t y = x - static_cast<int64_t>(pr.tiles_before[lo]) * units;
-    const int nt = pr.tiles_before[lo + 1] - pr.tiles_before[lo];
-    const int qt = nt - 1 - static_cast<int>(y / units);
-    const int unit = static_cast<int>(y % units);
+    const int qt = pr.tiles_before[lo + 1] - 1 - static_cast<int>(tile);  // the group's last tile first
     const int e = pr.by_rank[lo];
     it.idx = 0;
     it.g = p.h.head[(it.retr ? 0 : p.h.n_retr) + unit / per_kv];
@@ -172,24 +177,41 @@ __device__ __forceinline__ uint32_t elect_lane() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r;
 }
-// The products and commits of sm100.cuh, issued by the lanes with `lead` set only.
-__device__ __forceinline__ void tc_mma_ss_by(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// Products issued by the lanes with `lead` set only, several in one piece of assembly:
+// the issuing warp has 64 cycles per product, and a predicate or an address made anew
+// for each would cost a third of them. Descriptors advance by the operand's bytes / 16.
+//
+// D[tmem] = A[smem] * B[smem]^T over four steps of 16 (one 64-column block).
+__device__ __forceinline__ void tc_mma_ss4_by(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
         "setp.ne.b32 e, %5, 0;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts_by(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem] over four steps of 16 rows of B.
+__device__ __forceinline__ void tc_mma_ts4_by(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
         "setp.ne.b32 e, %5, 0;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
@@ -210,25 +232,48 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Adds to 32 columns of a row, from `col`, the infinities and NaN of the value rows
+// The keys that a row of the item sees.
+struct RowKeys {
+    RowVis vis;
+    int own0;  // first row of the row's prompt, in the group
+    __device__ __forceinline__ uint32_t bits(int k0) const { return chunk_bits_row(vis, k0) & ~bits_below32(own0 - k0); }
+};
+__device__ __forceinline__ RowKeys row_keys(const PackedPrefillParams& p, const PackItem& it, const int* first_row, int q) {
+    RowKeys r;
+    r.vis = row_visible(it.retr, 0, it.n, p.S, p.R, q);
+    r.own0 = 0;
+    if (it.p1 - it.p0 > 1) {
+        int lo = it.p0, up = it.p1 - 1;
+        while (lo < up) {
+            const int mid = (lo + up + 1) >> 1;
+            if (first_row[mid] <= it.start + q) lo = mid;
+            else up = mid - 1;
+        }
+        __syncwarp();
+        r.own0 = first_row[lo] - it.start;
+        r.vis.c_sink = it.retr ? 0 : r.own0 + p.S;
+    }
+    return r;
+}
+
+// Adds to 16 columns of a row, from `col`, the infinities and NaN of the value rows
 // that it sees among the tiles that were cleared of them: a visible row has a
 // positive weight, so the sum is that value whatever the weight is.
 template <typename Seen>
 __device__ __forceinline__ void add_odd_values(const PackedPrefillParams& p, const PackItem& it, int n, int col, Seen seen,
-                                               uint32_t (&r)[32]) {
-    const int last_row = (it.nb > 0 ? it.qb : it.qa) + kTileQ - 1;
+                                               uint32_t (&r)[16]) {
     const bf16* const v = p.v + static_cast<int64_t>(it.start) * p.kv_stride + it.g * p.D + col;
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
         const int row0 = key_row(it, j);
-        if (!(row0 + kTileK > it.qa || (!it.retr && row0 + kTileK > p.S && row0 <= last_row - p.R))) continue;
+        if (!seen_in_part(p, it, row0)) continue;
 #pragma unroll 1
         for (int k0 = row0; k0 < row0 + kTileK && k0 < it.n; k0 += 32)
 #pragma unroll 1
             for (uint32_t bits = seen(k0); bits; bits &= bits - 1) {
                 const bf16* const row = v + (k0 + __ffs(bits) - 1) * p.kv_stride;  // seen keys are rows of the group
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     const float x = __bfloat162float(row[i]);
                     if (!isfinite(x)) r[i] = __float_as_uint(__uint_as_float(r[i]) + x);
                 }
@@ -290,6 +335,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     uint32_t* const wrong = reinterpret_cast<uint32_t*>(smem + Lay::kMisc + 16);  // one bit per prompt: range not usable
     volatile int* const n_groups = reinterpret_cast<volatile int*>(smem + Lay::kMisc + 8);
     static_assert(kPagedMaxBatch <= 512, "16 words of bits");
+#pragma unroll 1
     for (int i0 = 0; i0 <= p.n; i0 += kPackThreads) {
         const int i = i0 + tid;
         bool bad = false;
@@ -306,9 +352,11 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         if (bits != 0 && lane == 0 && blockIdx.x == 0) atomicOr(p.err, kErrPagedArgument);
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = tid; i < p.n; i += kPackThreads) {
         // The first unusable prompt at i or behind; up to there the rows ascend.
         int stop = p.n;
+#pragma unroll 1
         for (int w = i >> 5; w <= (p.n - 1) >> 5; ++w) {
             const uint32_t bits = w == i >> 5 ? wrong[w] & (0xFFFFFFFFu << (i & 31)) : wrong[w];
             if (bits) {
@@ -326,22 +374,60 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         pr.next[i] = static_cast<uint16_t>(lo > i ? lo : i + 1);
     }
     __syncthreads();
-    if (tid == 0) {
-        int g = 0;
-        for (int i = 0; i < p.n; i = pr.next[i]) pr.first[g++] = static_cast<uint16_t>(i);
-        pr.first[g] = static_cast<uint16_t>(p.n);
-        *n_groups = g;
+    // The groups are what following `next` from prompt 0 meets. Jumps of 2, 4, 8, ..
+    // prompts' groups first, then back from the longest jump: a prompt that is met marks
+    // the one its jump leads to. Nine rounds instead of a chain of up to 512 reads.
+    {
+        uint16_t* const jump = reinterpret_cast<uint16_t*>(smem + Lay::kStage);  // [level][n + 1], in the output rows' place
+        const int n1 = p.n + 1;
+        int levels = 1;
+#pragma unroll 1
+        while ((1 << levels) < p.n) ++levels;
+#pragma unroll 1
+        for (int i = tid; i <= p.n; i += kPackThreads) jump[i] = i < p.n ? pr.next[i] : static_cast<uint16_t>(p.n);
+        uint32_t* const met = reinterpret_cast<uint32_t*>(smem + Lay::kStage + 15 * 1024);
+        if (tid < kPagedMaxBatch / 32 + 1) met[tid] = tid == 0 ? 1u : 0u;
+        __syncthreads();
+#pragma unroll 1
+        for (int l = 1; l < levels; ++l) {
+#pragma unroll 1
+            for (int i = tid; i <= p.n; i += kPackThreads) jump[l * n1 + i] = jump[(l - 1) * n1 + jump[(l - 1) * n1 + i]];
+            __syncthreads();
+        }
+#pragma unroll 1
+        for (int l = levels - 1; l >= 0; --l) {
+#pragma unroll 1
+            for (int i = tid; i < p.n; i += kPackThreads)
+                if ((met[i >> 5] >> (i & 31)) & 1u) {
+                    const int to = jump[l * n1 + i];
+                    atomicOr(&met[to >> 5], 1u << (to & 31));
+                }
+            __syncthreads();
+        }
+#pragma unroll 1
+        for (int i = tid; i <= p.n; i += kPackThreads) {
+            if (i < p.n && !((met[i >> 5] >> (i & 31)) & 1u)) continue;
+            int g = 0;  // groups before
+#pragma unroll 1
+            for (int w = 0; w < i >> 5; ++w) g += __popc(met[w]);
+            g += __popc(met[i >> 5] & ((1u << (i & 31)) - 1u));
+            pr.first[g] = static_cast<uint16_t>(i);
+            if (i == p.n) *n_groups = g;
+        }
     }
     __syncthreads();
     pr.n_groups = *n_groups;
+#pragma unroll 1
     for (int i = tid; i < pr.n_groups; i += kPackThreads) {
         const int f = pr.first[i];
         pr.len[i] = (wrong[f >> 5] >> (f & 31)) & 1u ? 0 : pr.row[pr.first[i + 1]] - pr.row[f];
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = tid; i < pr.n_groups; i += kPackThreads) {
         const int len = pr.len[i];
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < pr.n_groups; ++j) rank += pr.len[j] > len || (pr.len[j] == len && j < i);
         pr.by_rank[rank] = static_cast<uint16_t>(i);
     }
@@ -349,6 +435,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     if (warp == 0) {
         const int rows = (p.G & 1) ? 2 * kTileQ : kTileQ;
         int sum = 0;
+#pragma unroll 1
         for (int i0 = 0; i0 < pr.n_groups; i0 += 32) {
             const int i = i0 + lane;
             const int own = i < pr.n_groups ? query_tiles(pr.len[pr.by_rank[i]], rows) : 0;
@@ -367,8 +454,8 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int64_t n_items =
-        static_cast<int64_t>(pr.tiles_before[pr.n_groups]) * (p.h.n_retr + p.h.n_strm) * ((p.G & 1) ? p.G : p.G / 2);
+    const uint32_t n_items =
+        static_cast<uint32_t>(pr.tiles_before[pr.n_groups]) * (p.h.n_retr + p.h.n_strm) * ((p.G & 1) ? p.G : p.G / 2);
 
     // Item number `ord` of this CTA; false: none left, or a wait ran out.
     auto take_item = [&](int ord, PackItem& it) -> bool {
@@ -391,27 +478,35 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             tma_prefetch_desc(&maps.q);
             int published = 0;
             auto publish = [&](PackItem& it) -> bool {
-                const unsigned i = *abort_flag == 0 ? atomicAdd(p.work, 1u) : 0xFFFFFFFFu;
+                const uint32_t i = *abort_flag == 0 ? atomicAdd(p.work, 1u) : 0xFFFFFFFFu;
                 it.idx = -1;
                 if (i < n_items) it = pack_item(p, pr, i);
                 const int slot = published % kQueueSlots;
                 if (published >= kQueueSlots &&
-                    !mbar_wait(bar(kItemEmpty + slot), ((published / kQueueSlots) - 1) & 1, abort_flag))
+                    !mbar_wait_compact(bar(kItemEmpty + slot), ((published / kQueueSlots) - 1) & 1, abort_flag))
                     return false;
                 queue[slot] = it;
                 mbar_arrive(bar(kItemFull + slot));
                 ++published;
                 return true;
             };
-            int g = 0;  // K tiles issued
-            int q_loads = 0;
+            int g = 0;                // K and V tiles of the items before
+            int q_loads = 0, k_loads = 0;
+            int raw0 = 0, raw1 = 0;   // V tiles that the V warps go through, by stage
             PackItem it, after;
-            bool ok = publish(it);
+            it.idx = 0;
+            bool ok = true, first = true;
             while (ok && it.idx >= 0) {
                 ok = publish(after);
-                if (ok && q_loads >= 1) ok = mbar_wait(bar(kQEmpty), (q_loads - 1) & 1, abort_flag);
+                if (first) {  // nothing to load yet
+                    first = false;
+                    it = after;
+                    continue;
+                }
+                if (ok && q_loads >= 1) ok = mbar_wait_compact(bar(kQEmpty), (q_loads - 1) & 1, abort_flag);
                 if (!ok) break;
                 mbar_arrive_expect_tx(bar(kQFull), (it.nb > 0 ? 2 : 1) * Lay::kTile);
+#pragma unroll 1
                 for (int kb = 0; kb < Lay::kColBlocks; ++kb) {
                     tma_load_3d(sQ + kb * kTileBytesPerColBlock, &maps.q, bar(kQFull), kb * 64, it.head_a, it.start + it.qa);
                     if (it.nb > 0)
@@ -419,35 +514,56 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                                     it.start + it.qb);
                 }
                 ++q_loads;
+                // K and V tiles in turn: by the time a K stage is free the V stage before it is.
                 const int n = it.na > it.nb ? it.na : it.nb;
-                for (int j = 0; j < n; ++j, ++g) {
+#pragma unroll 1
+                for (int j = 0; ok && j < n; ++j, ++g) {
                     const int st = g & 1;
-                    if (g >= 2 && !mbar_wait(bar(kKEmpty + st), ((g >> 1) - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+                    const int row0 = key_row(it, j);
+                    if (g >= 2) ok = mbar_wait_compact(bar(kKEmpty + st), ((g >> 1) - 1) & 1, abort_flag);
+                    if (!ok) break;
                     mbar_arrive_expect_tx(bar(kKFull + st), Lay::kTile);
+#pragma unroll 1
                     for (int kb = 0; kb < Lay::kColBlocks; ++kb)
                         tma_load_3d(sK + st * Lay::kTile + kb * kTileBytesPerColBlock, &maps.k, bar(kKFull + st), kb * 64,
-                                    it.g, it.start + key_row(it, j));
+                                    it.g, it.start + row0);
+                    ++k_loads;
+                    if (g >= 2) ok = mbar_wait_compact(bar(kVEmpty + st), ((g >> 1) - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const bool part = seen_in_part(p, it, row0);
+                    const uint32_t full = bar((part ? kVRaw : kVFull) + st);
+                    mbar_arrive_expect_tx(full, Lay::kTile);
+#pragma unroll 1
+                    for (int kb = 0; kb < Lay::kColBlocks; ++kb)
+                        tma_load_3d(sV + st * Lay::kTile + kb * kTileBytesPerColBlock, &maps.v, full, kb * 64, it.g,
+                                    it.start + row0);
+                    if (part) ++(st ? raw1 : raw0);
+                    else mbar_arrive(full);  // for the second of the V warps
                 }
                 it = after;
             }
             if (!ok) give_up(p.err, abort_flag);
             // Every load issued lands before the CTA may exit.
-            for (int j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_wait(bar(kKFull + (j & 1)), (j >> 1) & 1, nullptr);
-            if (q_loads > 0) mbar_wait(bar(kQFull), (q_loads - 1) & 1, nullptr);
+            for (int j = k_loads > 2 ? k_loads - 2 : 0; j < k_loads; ++j) mbar_wait_compact(bar(kKFull + (j & 1)), (j >> 1) & 1, nullptr);
+            for (int st = 0; st < 2; ++st) {
+                const int raw = st ? raw1 : raw0;
+                if (raw > 0) mbar_wait_compact(bar(kVRaw + st), (raw - 1) & 1, nullptr);
+            }
+            for (int j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_wait_compact(bar(kVFull + (j & 1)), (j >> 1) & 1, abort_flag);
+            if (q_loads > 0) mbar_wait_compact(bar(kQFull), (q_loads - 1) & 1, nullptr);
         } else if (warp >= 10) {
-            // -------------------------------------------------------- V
-            // Warp 10 loads. A tile that some row of the item sees only in part (the
-            // diagonal, the window's edges, a group of prompts) is then gone through by
-            // both warps, half each, before the products may read it: a weight of zero
-            // must not meet an infinity or a NaN. Rows behind the group's end, which
-            // belong to other prompts or to nobody, become zero; a non-finite element
-            // becomes zero too and is counted for the rows that see it at the item's end.
+            // -------------------------------------------------------- V tiles seen in part
+            // A V tile that some row of the item sees only in part (the diagonal, the window's
+            // edges, a group of prompts) is gone through by both warps, 64 rows each, before
+            // the products may read it: a weight of zero must not meet an infinity or a NaN.
+            // Rows behind the group's end, which belong to other prompts or to nobody, become
+            // zero; a non-finite element becomes zero too and is counted for the rows that
+            // see it at the item's end.
             const int half = warp - 10;
-            int g = 0, raw = 0;
-            for (int ord = 0;; ++ord) {
+            int g = 0;
+            int raw0 = 0, raw1 = 0;  // such tiles so far, by stage
+            bool ok = true;
+            for (int ord = 0; ok; ++ord) {
                 PackItem it;
                 const bool more = take_item(ord, it);
                 __syncwarp();
@@ -456,72 +572,59 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 // The flag of four items ago, whose rows have long been written.
                 if (half == 0 && lane == 0) odd_values[(ord + 4) & 7] = 0;
                 const int n = it.na > it.nb ? it.na : it.nb;
-                const int last_row = (it.nb > 0 ? it.qb : it.qa) + kTileQ - 1;
-                bool ok = true;
                 for (int j = 0; j < n; ++j, ++g) {
                     const int st = g & 1;
-                    if (g >= 2 && !mbar_wait(bar(kVEmpty + st), ((g >> 1) - 1) & 1, abort_flag)) ok = false;
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
                     const int row0 = key_row(it, j);
-                    const bool part =
-                        row0 + kTileK > it.qa || (!it.retr && row0 + kTileK > p.S && row0 <= last_row - p.R);
-                    const uint32_t full = part ? bar(kVRaw + (raw & 1)) : bar(kVFull + st);
-                    if (half == 0 && lane == 0) {
-                        mbar_arrive_expect_tx(full, Lay::kTile);
-                        for (int kb = 0; kb < Lay::kColBlocks; ++kb)
-                            tma_load_3d(sV + st * Lay::kTile + kb * kTileBytesPerColBlock, &maps.v, full, kb * 64, it.g,
-                                        it.start + row0);
-                        if (!part) mbar_arrive(full);  // for the other warp
-                    }
-                    if (part) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kVRaw + (raw & 1)), (raw >> 1) & 1, nullptr));
-                        ++raw;
-                        const int valid = it.n - row0;
-                        bool odd = false;
-#pragma unroll
-                        for (int kb = 0; kb < Lay::kColBlocks; ++kb) {
-                            const uint32_t tile = sV + st * Lay::kTile + kb * kTileBytesPerColBlock + half * (64 * 128);
-                            uint32_t seen = 0;
-#pragma unroll 4
-                            for (int i = 0; i < 64 * 8 / 32; ++i) {
-                                const int row = half * 64 + i * 4 + (lane >> 3);
-                                const uint32_t a = tile + (i * 32 + lane) * 16;
-                                if (row < valid) {
-                                    const uint4 w = lds128(a);
-                                    // Bit 15 of a half word: its exponent bits are all ones.
-                                    seen |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                                            ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-                                } else {
-                                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0u) : "memory");
-                                }
-                            }
-                            if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0u)) {
-                                odd = true;
+                    if (!seen_in_part(p, it, row0)) continue;
+                    const int turn = st ? raw1++ : raw0++;
+                    ok = __all_sync(0xffffffffu, mbar_wait_compact(bar(kVRaw + st), turn & 1, abort_flag));
+                    if (!ok) break;
+                    const int valid = it.n - row0;
+                    bool odd = false;
 #pragma unroll 1
-                                for (int i = lane; i < 64 * 32; i += 32) {
-                                    uint32_t w;
-                                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(tile + i * 4));
-                                    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-                                    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-                                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(tile + i * 4), "r"(w) : "memory");
-                                }
+                    for (int kb = 0; kb < Lay::kColBlocks; ++kb) {
+                        const uint32_t tile = sV + st * Lay::kTile + kb * kTileBytesPerColBlock + half * (64 * 128);
+                        // 0 x w summed up: NaN in the end if any w was not finite.
+                        __nv_bfloat162 sum[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum[i] = __floats2bfloat162_rn(0.f, 0.f);
+                        const __nv_bfloat162 zero = sum[0];
+#pragma unroll 4
+                        for (int i = 0; i < 64 * 8 / 32; ++i) {
+                            const int row = half * 64 + i * 4 + (lane >> 3);
+                            const uint32_t a = tile + (i * 32 + lane) * 16;
+                            uint4 w = lds128(a);
+                            if (row >= valid) {
+                                w = make_uint4(0, 0, 0, 0);
+                                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0u) : "memory");
                             }
+                            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                sum[k] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&words[k]), zero, sum[k]);
                         }
-                        if (odd && lane == 0) odd_values[ord & 7] = 1;
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(kVFull + st));
+                        sum[0] = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+                        const float check = __low2float(sum[0]) + __high2float(sum[0]);
+                        if (__any_sync(0xffffffffu, !(check == 0.f))) {
+                            odd = true;
+#pragma unroll 1
+                            for (int i = lane; i < 64 * 32; i += 32) {
+                                uint32_t w;
+                                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(tile + i * 4));
+                                if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+                                if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(tile + i * 4), "r"(w) : "memory");
+                            }
+                            __syncwarp();
+                        }
                     }
-                }
-                if (!ok) {
-                    if (lane == 0) give_up(p.err, abort_flag);
-                    break;
+                    if (odd && lane == 0) odd_values[ord & 7] = 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kVFull + st));
                 }
             }
-            for (int j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_wait(bar(kVFull + (j & 1)), (j >> 1) & 1, abort_flag);
+            if (!ok && lane == 0) give_up(p.err, abort_flag);
         } else if (warp == 9) {
             // -------------------------------------------------------- products
             // The whole warp walks the loop and one elected lane issues: control flow and
@@ -532,86 +635,97 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             const uint32_t lead = elect_lane();
             const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
             const uint64_t dv = smem_desc_sw128(sV, kTileBytesPerColBlock, 1024);
-            int g = 0;               // K/V tiles of the items before
+            int g = -1;              // key tile that the item starts with; the first is 0
             int count_a = 0, count_b = 0;  // products PV of each tile so far
             int items_a = 0, items_b = 0;  // items that had the tile so far
             bool ok = true;
-            for (int ord = 0; ok; ++ord) {
+            // S(x) = Q(x) K(t)^T for the CTA's key tile t; `last`: the last product to read it,
+            // `last_q`: and the last to read Q.
+            auto qk = [&](auto x_, int t, bool wait, bool last, bool last_q) {
+                constexpr int x = decltype(x_)::value;
+                const int st = t & 1;
+                if (wait && !__all_sync(0xffffffffu, mbar_wait_compact(bar(kKFull + st), (t >> 1) & 1, abort_flag))) return false;
+                tc_fence_after();
+                const uint64_t q = dq + x * (Lay::kTile >> 4), k = dk + st * (Lay::kTile >> 4);
+#pragma unroll
+                for (int kb = 0; kb < D / 64; ++kb)
+                    tc_mma_ss4_by(lead, tmem + x * kTileK, q + kb * (kTileBytesPerColBlock >> 4),
+                                  k + kb * (kTileBytesPerColBlock >> 4), idesc_qk, kb);
+                tc_commit_by(lead, bar(kSFull + x));
+                if (last) {
+                    tc_commit_by(lead, bar(kKEmpty + st));
+                    if (last_q) tc_commit_by(lead, bar(kQEmpty));
+                }
+                return true;
+            };
+            // O(x) += P(x) V(t); `first`: of the item.
+            auto pv = [&](auto x_, int t, bool wait, bool last, bool first, int count, int items) {
+                constexpr int x = decltype(x_)::value;
+                const int st = t & 1;
+                if (wait && !__all_sync(0xffffffffu, mbar_wait_compact(bar(kVFull + st), (t >> 1) & 1, abort_flag))) return false;
+                if (first && items > 0 &&
+                    !__all_sync(0xffffffffu, mbar_wait_compact(bar(kOEmpty + x), (items - 1) & 1, abort_flag)))
+                    return false;
+                const uint64_t vt = dv + st * (Lay::kTile >> 4);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_compact(bar(kPFull + 2 * x + half), count & 1, abort_flag))) return false;
+                    tc_fence_after();
+                    tc_mma_ts4_by(lead, tmem + kTmemO + x * 128, tmem + x * kTileK + half * 32, vt + half * 4 * (2048 >> 4),
+                                  idesc_pv, first && half == 0 ? 0u : 1u);
+                }
+                tc_commit_by(lead, bar(kODone + x));
+                if (last) tc_commit_by(lead, bar(kVEmpty + st));
+                return true;
+            };
+            constexpr std::integral_constant<int, 0> A{};
+            constexpr std::integral_constant<int, 1> B{};
+            int ord = 0, na = 0, nb = 0;
+            // The next item's tile counts (0: none left), its queries waited for.
+            auto next_item = [&](int& a, int& b) {
                 PackItem it;
                 const bool more = take_item(ord, it);
                 __syncwarp();
                 if (lead) free_item(ord);
-                if (!__all_sync(0xffffffffu, more)) break;
-                const int na = __shfl_sync(0xffffffffu, it.na, 0), nb = __shfl_sync(0xffffffffu, it.nb, 0);
-                const int n = na > nb ? na : nb;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFull), ord & 1, abort_flag));
-                // S(x) = Q(x) K(j)^T; `last`: the last to read the K tile.
-                auto qk = [&](auto x_, int j, bool wait, bool last) {
-                    constexpr int x = decltype(x_)::value;
-                    const int st = (g + j) & 1;
-                    if (wait && !__all_sync(0xffffffffu, mbar_wait(bar(kKFull + st), ((g + j) >> 1) & 1, abort_flag))) return false;
-                    tc_fence_after();
-                    const uint64_t q = dq + x * (Lay::kTile >> 4), k = dk + st * (Lay::kTile >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * kTileBytesPerColBlock + (kk & 3) * 32) >> 4;
-                        tc_mma_ss_by(lead, tmem + x * kTileK, q + off, k + off, idesc_qk, kk > 0 ? 1u : 0u);
-                    }
-                    tc_commit_by(lead, bar(kSFull + x));
-                    if (last) {
-                        tc_commit_by(lead, bar(kKEmpty + st));
-                        if (j + 1 == n) tc_commit_by(lead, bar(kQEmpty));
-                    }
-                    return true;
-                };
-                // O(x) += P(x) V(j); `last`: the last to read the V tile.
-                auto pv = [&](auto x_, int j, bool wait, bool last, int count, int items) {
-                    constexpr int x = decltype(x_)::value;
-                    const int st = (g + j) & 1;
-                    if (wait && !__all_sync(0xffffffffu, mbar_wait(bar(kVFull + st), ((g + j) >> 1) & 1, abort_flag))) return false;
-                    if (j == 0 && items > 0 &&
-                        !__all_sync(0xffffffffu, mbar_wait(bar(kOEmpty + x), (items - 1) & 1, abort_flag)))
-                        return false;
-                    const uint64_t vt = dv + st * (Lay::kTile >> 4);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (!__all_sync(0xffffffffu, mbar_wait(bar(kPFull + 2 * x + half), count & 1, abort_flag))) return false;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4) {
-                            const int kk = half * 4 + k4;
-                            tc_mma_ts_by(lead, tmem + kTmemO + x * 128, tmem + x * kTileK + kk * 8, vt + kk * (2048 >> 4),
-                                         idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-                        }
-                    }
-                    tc_commit_by(lead, bar(kODone + x));
-                    if (last) tc_commit_by(lead, bar(kVEmpty + st));
-                    return true;
-                };
-                constexpr std::integral_constant<int, 0> A{};
-                constexpr std::integral_constant<int, 1> B{};
-                // The tiles' lists differ by one tile at most, or one is empty.
-                if (ok && na > 0) ok = qk(A, 0, true, nb == 0);
-                if (ok && nb > 0) ok = qk(B, 0, na == 0, true);
+                a = b = 0;
+                if (!__all_sync(0xffffffffu, more)) return;
+                a = __shfl_sync(0xffffffffu, it.na, 0);
+                b = __shfl_sync(0xffffffffu, it.nb, 0);
+                ok = __all_sync(0xffffffffu, mbar_wait_compact(bar(kQFull), ord & 1, abort_flag));
+                ++ord;
+            };
+            // Per key tile PV(A), QK(A) of the next tile, PV(B), QK(B): the next tile behind an
+            // item's last is the next item's first, so that its scores are there when the
+            // softmax has written the item's rows. Every QK of the item is issued by then, and
+            // its queries have been replaced. A's list is B's without its last tile, or as
+            // long; there may be no B. Before the first item: one tile of nothing.
+            int n = 1;
+            while (ok && n > 0) {
+                int next_a = na, next_b = nb, next_n = n;
+#pragma unroll 1
                 for (int j = 0; ok && j < n; ++j) {
-                    if (j < na) {
-                        ok = pv(A, j, true, j >= nb, count_a, items_a);
-                        ++count_a;
-                        if (ok && j + 1 < na) ok = qk(A, j + 1, true, j + 1 >= nb);
+                    const int t = g + j;
+                    const bool turn = j + 1 == n;  // the next tile is the next item's
+                    if (j < na) ok = pv(A, t, true, j >= nb, j == 0, count_a++, items_a);
+                    if (ok && turn) {
+                        next_item(next_a, next_b);
+                        next_n = next_a > next_b ? next_a : next_b;
                     }
-                    if (ok && j < nb) {
-                        ok = pv(B, j, j >= na, true, count_b, items_b);
-                        ++count_b;
-                        if (ok && j + 1 < nb) ok = qk(B, j + 1, j + 1 >= na, true);
-                    }
+                    const int k = turn ? 0 : j + 1;  // the next tile's number in its item
+                    if (ok && k < next_a && (turn || k < na)) ok = qk(A, t + 1, true, k >= next_b, k + 1 == next_n);
+                    if (ok && j < nb) ok = pv(B, t, j >= na, true, j == 0, count_b++, items_b);
+                    if (ok && k < next_b && (turn || k < nb)) ok = qk(B, t + 1, k >= next_a, true, k + 1 == next_n);
                 }
                 items_a += na > 0;
                 items_b += nb > 0;
                 g += n;
+                na = next_a;
+                nb = next_b;
+                n = next_n;
             }
             if (!ok && lead) give_up(p.err, abort_flag);
             tc_commit_by(lead, bar(kDrain));  // every product issued has completed before TMEM is released
-            mbar_wait(bar(kDrain), 0, nullptr);
+            mbar_wait_compact(bar(kDrain), 0, nullptr);
         }
         __syncwarp();
     } else {
@@ -636,22 +750,9 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             if (n == 0) continue;
             const int q0 = x ? it.qb : it.qa;
             const int head = x ? it.head_b : it.head_a;
-            RowVis vis = row_visible(it.retr, 0, it.n, p.S, p.R, q0 + row);
-            int own0 = 0;  // first row of this row's prompt, in the group
             const bool single = it.p1 - it.p0 == 1;
-            if (!single) {
-                int lo = it.p0, up = it.p1 - 1;
-                while (lo < up) {
-                    const int mid = (lo + up + 1) >> 1;
-                    if (pr.row[mid] <= it.start + row) lo = mid;
-                    else up = mid - 1;
-                }
-                __syncwarp();
-                own0 = pr.row[lo] - it.start;
-                vis.c_sink = it.retr ? 0 : own0 + p.S;
-            }
-            // The 32 keys from k0 that this row sees.
-            auto seen_bits = [&](int k0) { return chunk_bits_row(vis, k0) & ~bits_below32(own0 - k0); };
+            const RowKeys keys = row_keys(p, it, pr.row, q0 + row);
+            auto seen_bits = [&](int k0) { return keys.bits(k0); };
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < n; ++j, ++count) {
                 if (!__all_sync(0xffffffffu, mbar_wait(bar(kSFull + x), count & 1, abort_flag))) {
@@ -659,42 +760,62 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
-                tc_wait_ld();
                 const int row0 = key_row(it, j);
                 // The tile in four runs of 32 keys: what the warp's 32 rows [r0, r0 + 31] see
-                // of each is all of it, nothing, or a part, by comparisons that are the same
-                // for the whole warp. Only parts are masked element by element; a run that
-                // no row sees costs nothing but a zero P.
-                const int r0 = q0 + quarter * 32;
-                uint32_t none = 0;  // bit c: nothing of run c is seen
+                // of each is all of it, nothing, or a part: one bit per run, the same for the
+                // whole warp. Only parts are masked element by element; a run that no row sees
+                // costs nothing but a zero P.
+                uint32_t none, all;
+                {
+                    auto below = [](int x) { return (1u << (x < 0 ? 0 : x > 4 ? 4 : x)) - 1u; };
+                    const int d = (q0 + quarter * 32 - row0) >> 5;  // the diagonal's run
+                    none = ~below(d + 1);
+                    all = single ? below(d) : 0u;
+                    if (single && !it.retr) {
+                        const int e = q0 + quarter * 32 - p.R - row0;  // keys <= e are outside all rows' windows,
+                        const int sk = p.S - row0;                     // keys > e + 31 inside all; keys < sk are sinks
+                        all &= ~below(((e + 31) >> 5) + 1) | below(sk >> 5);
+                        none |= below((e + 1) >> 5) & ~below((sk + 31) >> 5);
+                    }
+                    all = __shfl_sync(0xffffffffu, all, 0);
+                    none = __shfl_sync(0xffffffffu, none, 0);
+                }
+                // Two versions of what follows. A tile seen whole is handled at once, unrolled
+                // over its 128 columns. Any other is handled run by run, each run read from
+                // TMEM twice (for the maximum, for the weights), which costs next to nothing,
+                // and in a quarter of the code: the roles' loops have to fit the instruction
+                // cache together.
+                const bool whole = all == 15u;
+                uint32_t s[4][32];
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 auto max_of = [&](const uint32_t (&run)[32]) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 2)
                         m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], __uint_as_float(run[i]), __uint_as_float(run[i + 1]));
                 };
-                if (row0 + kTileK <= q0 && (it.retr || row0 + kTileK <= p.S || row0 > q0 + kTileQ - 1 - p.R)) {
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+                    tc_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) max_of(s[c]);
                 } else {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        const int k0 = row0 + 32 * c, k1 = k0 + 31;
-                        if (k0 > r0 + 31 || (!it.retr && single && k0 >= p.S && k1 <= r0 - p.R)) {
-                            none |= 1u << c;
-                            continue;
-                        }
-                        if (!(k1 <= r0 && single && (it.retr || k1 < p.S || k0 > r0 + 31 - p.R))) {
-                            const uint32_t bits = seen_bits(k0);
+                        if ((none >> c) & 1u) continue;
+                        uint32_t run[32];
+                        tmem_ld32(tS + c * 32, run);
+                        tc_wait_ld();
+                        if (!((all >> c) & 1u)) {
+                            const uint32_t bits = seen_bits(row0 + 32 * c);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (!((bits >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
+                                if (!((bits >> k) & 1u)) run[k] = 0xFF800000u;  // -inf
+                            tmem_st32(tS + c * 32, run);  // for the second pass
                         }
-                        max_of(s[c]);
+                        max_of(run);
                     }
+                    tc_wait_st();
                 }
                 const float mt = fmax3(fmaxf(m[0], m[1]), m[2], m[3]) * p.scale_log2;
                 float factor = 1.f;
@@ -722,37 +843,48 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;
                 const uint64_t negm = f2pack(-m_use, -m_use);
                 uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-                // Weights, in two versions: with a test per run the compiler cannot overlap
-                // the runs, which costs a fully seen tile 8 %.
-                auto weights = [&](auto some_) {
+                // P of a run goes over S columns that have been read: 16 c .. of run c and before.
+                auto weights_of = [&](const uint32_t (&run)[32], int c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float e0, e1;
+                        f2unpack(ffma2(f2pack(__uint_as_float(run[i]), __uint_as_float(run[i + 1])), scale2, negm), e0, e1);
+                        const float p0 = fast_exp2(e0), p1 = fast_exp2(e1);
+                        acc[(i >> 1) & 1] = fadd2(acc[(i >> 1) & 1], f2pack(p0, p1));
+                        pk[i >> 1] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st16(tS + c * 16, pk);
+                };
+                auto hand_over = [&](int half) {  // 64 keys' weights are written
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kPFull + 2 * x + half));
+                };
+                if (whole) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t pk[16];
-                        if (decltype(some_)::value && ((none >> c) & 1u)) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) pk[i] = 0u;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float e0, e1;
-                                f2unpack(ffma2(f2pack(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), scale2, negm),
-                                         e0, e1);
-                                const float p0 = fast_exp2(e0), p1 = fast_exp2(e1);
-                                acc[(i >> 1) & 1] = fadd2(acc[(i >> 1) & 1], f2pack(p0, p1));
-                                pk[i >> 1] = pack_bf16x2(p0, p1);
-                            }
-                        }
-                        tmem_st16(tS + c * 16, pk);  // every S column has been read
-                        if (c & 1) {
-                            tc_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(kPFull + 2 * x + (c >> 1)));
-                        }
+                        weights_of(s[c], c);
+                        if (c & 1) hand_over(c >> 1);
                     }
-                };
-                if (none == 0) weights(std::false_type{});
-                else weights(std::true_type{});
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        if ((none >> c) & 1u) {
+                            uint32_t zero[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) zero[i] = 0u;
+                            tmem_st16(tS + c * 16, zero);
+                        } else {
+                            uint32_t run[32];
+                            tmem_ld32(tS + c * 32, run);
+                            tc_wait_ld();
+                            weights_of(run, c);
+                        }
+                        if (c & 1) hand_over(c >> 1);
+                    }
+                }
                 float a0, a1;
                 f2unpack(fadd2(acc[0], acc[1]), a0, a1);
                 l_run = l_run * factor + (a0 + a1);
@@ -770,13 +902,26 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             const uint32_t stage = base + Lay::kStage + warp * 2048;
             const int rows = it.n - (q0 + quarter * 32);  // of the warp that exist
             bf16* const o = p.out + (static_cast<int64_t>(it.start) + q0 + quarter * 32) * p.out_stride + head * D;
-            const bool odd = odd_values[ord & 7] != 0;
+            if (odd_values[ord & 7] != 0) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t r[16];
+                    tmem_ld16(tO + c * 16, r);
+                    tc_wait_ld();
+                    add_odd_values(p, it, n, c * 16, seen_bits, r);
+                    tmem_st16(tO + c * 16, r);
+                }
+                tc_wait_st();
+            }
+            const uint32_t put = stage + lane * 64, swz = (lane >> 1) & 3;
+            const uint32_t get = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+            bf16* dst = o + (lane >> 2) * p.out_stride + (lane & 3) * 8;
+            const int64_t step = 8 * p.out_stride;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c, dst += 32) {
                 uint32_t r[32];
                 tmem_ld32(tO + c * 32, r);
                 tc_wait_ld();
-                if (odd) add_odd_values(p, it, n, c * 32, seen_bits, r);
                 if (c + 1 == D / 32) {
                     tc_fence_before();
                     __syncwarp();
@@ -784,7 +929,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t a = stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4);
+                    const uint32_t a = put + ((i ^ swz) << 4);
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a),
                                  "r"(pack_bf16x2(__uint_as_float(r[8 * i]) * inv, __uint_as_float(r[8 * i + 1]) * inv)),
                                  "r"(pack_bf16x2(__uint_as_float(r[8 * i + 2]) * inv, __uint_as_float(r[8 * i + 3]) * inv)),
@@ -795,9 +940,8 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int rr = i * 8 + (lane >> 2), ch = lane & 3;
-                    const uint4 w = lds128(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
-                    if (rr < rows) *reinterpret_cast<uint4*>(o + rr * p.out_stride + c * 32 + ch * 8) = w;
+                    const uint4 w = lds128(get + i * 512);  // rows lane / 4, 8 apart: the same swizzle
+                    if ((lane >> 2) + i * 8 < rows) *reinterpret_cast<uint4*>(dst + i * step) = w;
                 }
                 __syncwarp();
             }

@@ -80,6 +80,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const v
     }
 }
 
+// The same wait for kernels with many of them: what comes after the first try is one
+// function, not a copy at every wait. (A kernel whose roles' loops together outgrow
+// the instruction cache refetches them all the time.)
+static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+    return mbar_wait(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool mbar_wait_compact(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_on(bar, parity, abort_flag);
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

@@ -281,6 +281,149 @@ __device__ __forceinline__ void add_odd_values(const PackedPrefillParams& p, con
     }
 }
 
+// Groups of neighbouring prompts, their ranks by length and the query tiles before
+// each. The whole CTA; `scratch`: 16 KB that nobody uses yet.
+__device__ __forceinline__ void group_prompts(const PackedPrefillParams& p, Prompts& pr, const uint32_t* wrong,
+                                              volatile int* n_groups, uint8_t* scratch, int rows_per_tile) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+#pragma unroll 1
+    for (int i = tid; i < p.n; i += kPackThreads) {
+        // The first unusable prompt at i or behind; up to there the rows ascend.
+        int stop = p.n;
+#pragma unroll 1
+        for (int w = i >> 5; w <= (p.n - 1) >> 5; ++w) {
+            const uint32_t bits = w == i >> 5 ? wrong[w] & (0xFFFFFFFFu << (i & 31)) : wrong[w];
+            if (bits) {
+                stop = w * 32 + __ffs(bits) - 1;
+                break;
+            }
+        }
+        // The last j with all of [i, j) in one tile.
+        int lo = i < stop ? i : stop, up = stop;
+        while (lo < up) {
+            const int mid = (lo + up + 1) >> 1;
+            if (pr.row[mid] - pr.row[i] <= kTileQ) lo = mid;
+            else up = mid - 1;
+        }
+        pr.next[i] = static_cast<uint16_t>(lo > i ? lo : i + 1);
+    }
+    __syncthreads();
+    // The groups are what following `next` from prompt 0 meets. One thread takes jumps
+    // of eight groups, then each place that it met is followed for eight groups by a
+    // thread of its own: a chain of up to 512 reads becomes one of 64.
+    const int n1 = p.n + 1;
+    uint16_t* const jump[2] = {reinterpret_cast<uint16_t*>(scratch), reinterpret_cast<uint16_t*>(scratch) + n1};
+    uint16_t* const met = jump[1] + n1;  // [65]
+    volatile int* const n_met = reinterpret_cast<volatile int*>(scratch + 8 * 1024);
+    volatile int* const n_long = n_met + 1;
+    uint32_t* const is_long = reinterpret_cast<uint32_t*>(scratch + 8 * 1024 + 64);   // a bit per group
+    uint32_t* const is_short = is_long + kPagedMaxBatch / 32;
+#pragma unroll 1
+    for (int i = tid; i <= p.n; i += kPackThreads) {  // two groups on
+        const int k = i < p.n ? pr.next[i] : p.n;
+        jump[0][i] = k < p.n ? pr.next[k] : static_cast<uint16_t>(p.n);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i <= p.n; i += kPackThreads) jump[1][i] = jump[0][jump[0][i]];
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i <= p.n; i += kPackThreads) jump[0][i] = jump[1][jump[1][i]];
+    __syncthreads();
+    if (tid == 0) {
+        int m = 0;
+#pragma unroll 1
+        for (int i = 0; i < p.n; i = jump[0][i]) met[m++] = static_cast<uint16_t>(i);
+        *n_met = m;
+    }
+    __syncthreads();
+    if (tid < *n_met) {
+        int g = tid * 8, i = met[tid];
+#pragma unroll 1
+        for (int k = 0; k < 8 && i < p.n; ++k, ++g) {
+            pr.first[g] = static_cast<uint16_t>(i);
+            i = pr.next[i];
+        }
+        if (i >= p.n) {  // the last of them
+            pr.first[g] = static_cast<uint16_t>(p.n);
+            *n_groups = g;
+        }
+    }
+    __syncthreads();
+    pr.n_groups = *n_groups;
+    // Groups of more than one tile come first, longest first; those of one tile and empty
+    // ones follow in order.
+#pragma unroll 1
+    for (int i0 = 0; i0 < pr.n_groups; i0 += kPackThreads) {
+        const int i = i0 + tid;
+        int len = 0;
+        if (i < pr.n_groups) {
+            const int f = pr.first[i];
+            len = (wrong[f >> 5] >> (f & 31)) & 1u ? 0 : pr.row[pr.first[i + 1]] - pr.row[f];
+            pr.len[i] = len;
+        }
+        const uint32_t l = __ballot_sync(0xffffffffu, len > kTileQ), s = __ballot_sync(0xffffffffu, len > 0 && len <= kTileQ);
+        if (lane == 0 && i / 32 < kPagedMaxBatch / 32) {
+            is_long[i / 32] = l;
+            is_short[i / 32] = s;
+        }
+    }
+    __syncthreads();
+    int longs = 0, shorts = 0;
+#pragma unroll 1
+    for (int w = 0; w <= (pr.n_groups - 1) >> 5; ++w) {
+        longs += __popc(is_long[w]);
+        shorts += __popc(is_short[w]);
+    }
+#pragma unroll 1
+    for (int i = tid; i < pr.n_groups; i += kPackThreads) {
+        const uint32_t below = (1u << (i & 31)) - 1u;
+        int long_before = __popc(is_long[i >> 5] & below), short_before = __popc(is_short[i >> 5] & below);
+#pragma unroll 1
+        for (int w = 0; w < i >> 5; ++w) {
+            long_before += __popc(is_long[w]);
+            short_before += __popc(is_short[w]);
+        }
+        if ((is_long[i >> 5] >> (i & 31)) & 1u) jump[0][long_before] = static_cast<uint16_t>(i);  // the list of long ones
+        else if ((is_short[i >> 5] >> (i & 31)) & 1u) pr.by_rank[longs + short_before] = static_cast<uint16_t>(i);
+        else pr.by_rank[longs + shorts + (i - long_before - short_before)] = static_cast<uint16_t>(i);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = tid; k < longs; k += kPackThreads) {
+        const int len = pr.len[jump[0][k]];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < longs; ++j) {
+            const int other = pr.len[jump[0][j]];
+            rank += other > len || (other == len && j < k);
+        }
+        pr.by_rank[rank] = jump[0][k];
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int sum = 0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < longs; i0 += 32) {
+            const int i = i0 + lane;
+            const int own = i < longs ? query_tiles(pr.len[pr.by_rank[i]], rows_per_tile) : 0;
+            int t = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, t, o);
+                t += lane >= o ? a : 0;
+            }
+            if (i < longs) pr.tiles_before[i] = sum + t - own;
+            sum += __shfl_sync(0xffffffffu, t, 31);
+        }
+        if (lane == 0) *n_long = sum;  // tiles of the long groups
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int r = longs + tid; r <= pr.n_groups; r += kPackThreads)
+        pr.tiles_before[r] = *n_long + min(r - longs, shorts);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPackThreads, 1)
     prefill_packed_kernel(const __grid_constant__ PackedPrefillParams p, const __grid_constant__ PackedMaps maps) {
@@ -335,6 +478,8 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     uint32_t* const wrong = reinterpret_cast<uint32_t*>(smem + Lay::kMisc + 16);  // one bit per prompt: range not usable
     volatile int* const n_groups = reinterpret_cast<volatile int*>(smem + Lay::kMisc + 8);
     static_assert(kPagedMaxBatch <= 512, "16 words of bits");
+    grid_dependency_wait();
+    grid_launch_dependents();
 #pragma unroll 1
     for (int i0 = 0; i0 <= p.n; i0 += kPackThreads) {
         const int i = i0 + tid;
@@ -352,103 +497,19 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         if (bits != 0 && lane == 0 && blockIdx.x == 0) atomicOr(p.err, kErrPagedArgument);
     }
     __syncthreads();
-#pragma unroll 1
-    for (int i = tid; i < p.n; i += kPackThreads) {
-        // The first unusable prompt at i or behind; up to there the rows ascend.
-        int stop = p.n;
-#pragma unroll 1
-        for (int w = i >> 5; w <= (p.n - 1) >> 5; ++w) {
-            const uint32_t bits = w == i >> 5 ? wrong[w] & (0xFFFFFFFFu << (i & 31)) : wrong[w];
-            if (bits) {
-                stop = w * 32 + __ffs(bits) - 1;
-                break;
-            }
+    const int rows_per_tile = (p.G & 1) ? 2 * kTileQ : kTileQ;
+    if (p.n == 1) {  // one prompt: none of the below
+        pr.n_groups = 1;
+        if (tid == 0) {
+            pr.len[0] = (wrong[0] & 1u) ? 0 : pr.row[1] - pr.row[0];
+            pr.first[0] = 0;
+            pr.first[1] = 1;
+            pr.by_rank[0] = 0;
+            pr.tiles_before[0] = 0;
+            pr.tiles_before[1] = query_tiles(pr.len[0], rows_per_tile);
         }
-        // The last j with all of [i, j) in one tile.
-        int lo = i < stop ? i : stop, up = stop;
-        while (lo < up) {
-            const int mid = (lo + up + 1) >> 1;
-            if (pr.row[mid] - pr.row[i] <= kTileQ) lo = mid;
-            else up = mid - 1;
-        }
-        pr.next[i] = static_cast<uint16_t>(lo > i ? lo : i + 1);
-    }
-    __syncthreads();
-    // The groups are what following `next` from prompt 0 meets. Jumps of 2, 4, 8, ..
-    // prompts' groups first, then back from the longest jump: a prompt that is met marks
-    // the one its jump leads to. Nine rounds instead of a chain of up to 512 reads.
-    {
-        uint16_t* const jump = reinterpret_cast<uint16_t*>(smem + Lay::kStage);  // [level][n + 1], in the output rows' place
-        const int n1 = p.n + 1;
-        int levels = 1;
-#pragma unroll 1
-        while ((1 << levels) < p.n) ++levels;
-#pragma unroll 1
-        for (int i = tid; i <= p.n; i += kPackThreads) jump[i] = i < p.n ? pr.next[i] : static_cast<uint16_t>(p.n);
-        uint32_t* const met = reinterpret_cast<uint32_t*>(smem + Lay::kStage + 15 * 1024);
-        if (tid < kPagedMaxBatch / 32 + 1) met[tid] = tid == 0 ? 1u : 0u;
-        __syncthreads();
-#pragma unroll 1
-        for (int l = 1; l < levels; ++l) {
-#pragma unroll 1
-            for (int i = tid; i <= p.n; i += kPackThreads) jump[l * n1 + i] = jump[(l - 1) * n1 + jump[(l - 1) * n1 + i]];
-            __syncthreads();
-        }
-#pragma unroll 1
-        for (int l = levels - 1; l >= 0; --l) {
-#pragma unroll 1
-            for (int i = tid; i < p.n; i += kPackThreads)
-                if ((met[i >> 5] >> (i & 31)) & 1u) {
-                    const int to = jump[l * n1 + i];
-                    atomicOr(&met[to >> 5], 1u << (to & 31));
-                }
-            __syncthreads();
-        }
-#pragma unroll 1
-        for (int i = tid; i <= p.n; i += kPackThreads) {
-            if (i < p.n && !((met[i >> 5] >> (i & 31)) & 1u)) continue;
-            int g = 0;  // groups before
-#pragma unroll 1
-            for (int w = 0; w < i >> 5; ++w) g += __popc(met[w]);
-            g += __popc(met[i >> 5] & ((1u << (i & 31)) - 1u));
-            pr.first[g] = static_cast<uint16_t>(i);
-            if (i == p.n) *n_groups = g;
-        }
-    }
-    __syncthreads();
-    pr.n_groups = *n_groups;
-#pragma unroll 1
-    for (int i = tid; i < pr.n_groups; i += kPackThreads) {
-        const int f = pr.first[i];
-        pr.len[i] = (wrong[f >> 5] >> (f & 31)) & 1u ? 0 : pr.row[pr.first[i + 1]] - pr.row[f];
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int i = tid; i < pr.n_groups; i += kPackThreads) {
-        const int len = pr.len[i];
-        int rank = 0;
-#pragma unroll 4
-        for (int j = 0; j < pr.n_groups; ++j) rank += pr.len[j] > len || (pr.len[j] == len && j < i);
-        pr.by_rank[rank] = static_cast<uint16_t>(i);
-    }
-    __syncthreads();
-    if (warp == 0) {
-        const int rows = (p.G & 1) ? 2 * kTileQ : kTileQ;
-        int sum = 0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < pr.n_groups; i0 += 32) {
-            const int i = i0 + lane;
-            const int own = i < pr.n_groups ? query_tiles(pr.len[pr.by_rank[i]], rows) : 0;
-            int t = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(0xffffffffu, t, o);
-                if (lane >= o) t += a;
-            }
-            if (i < pr.n_groups) pr.tiles_before[i] = sum + t - own;
-            sum += __shfl_sync(0xffffffffu, t, 31);
-        }
-        if (lane == 0) pr.tiles_before[pr.n_groups] = sum;
+    } else {
+        group_prompts(p, pr, wrong, n_groups, smem + Lay::kStage, rows_per_tile);
     }
     tc_fence_before();
     __syncthreads();
@@ -478,7 +539,9 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             tma_prefetch_desc(&maps.q);
             int published = 0;
             auto publish = [&](PackItem& it) -> bool {
-                const uint32_t i = *abort_flag == 0 ? atomicAdd(p.work, 1u) : 0xFFFFFFFFu;
+                // The first item is the CTA's own number; the counter hands out the ones behind.
+                const uint32_t i = published == 0 ? blockIdx.x
+                                   : *abort_flag == 0 ? gridDim.x + atomicAdd(p.work, 1u) : 0xFFFFFFFFu;
                 it.idx = -1;
                 if (i < n_items) it = pack_item(p, pr, i);
                 const int slot = published % kQueueSlots;
@@ -966,9 +1029,21 @@ cudaError_t launch_d(const PackedPrefillParams& p, const PackedMaps& m, int num_
     static SmemLimitOnce limit;
     const cudaError_t e = limit.apply(reinterpret_cast<const void*>(&prefill_packed_kernel<D>), kMaxSmem);
     if (e != cudaSuccess) return e;
-    // The whole shared memory for every D: one CTA per SM, so none waits for TMEM.
-    prefill_packed_kernel<D><<<static_cast<unsigned>(num_sms), kPackThreads, kMaxSmem, s>>>(p, m);
-    return cudaGetLastError();
+    // No more CTAs than there can be items; the whole shared memory for every D: one CTA
+    // per SM, so none waits for TMEM.
+    const int64_t units = (p.h.n_retr + p.h.n_strm) * ((p.G & 1) ? p.G : p.G / 2);
+    const int64_t items = ((p.n_rows + kTileQ - 1) / kTileQ + p.n) * units;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items < num_sms ? items : num_sms));
+    cfg.blockDim = dim3(kPackThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, &prefill_packed_kernel<D>, p, m);
 }
 
 }  // namespace

@@ -556,8 +556,8 @@ class PagedCache:
         if n is not None and rows != n:
             raise ValueError(f"{name}: expected {n} rows, got {rows}")
         s = t.stride()
-        if rows and (s[2] != 1 or (heads > 1 and s[1] != d)):
-            raise ValueError(f"{name}: a row must be dense, got strides {s}")
+        if rows and (s[2] != 1 or (heads > 1 and s[1] != d) or (rows > 1 and s[0] < heads * d)):
+            raise ValueError(f"{name}: rows must be dense and must not overlap, got strides {s}")
         return t.data_ptr(), (s[0] if rows > 1 else 0)
 
     def _kv(self, k, v, n):

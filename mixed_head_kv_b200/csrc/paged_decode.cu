@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     int16_t* heads = reinterpret_cast<int16_t*>(smem + L::kHeads);
     if (tid < p.h.n_retr + p.h.n_strm) heads[tid] = p.h.head[tid];
-    if (warp == kWarps && lane < 4) tma_prefetch_desc(lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.wk : &maps.wv);
+    if (warp == kWarps && lane < 4 && (lane < 2 ? p.v.r_all : p.v.s_all) > 0)  // a pool without heads has no map
+        tma_prefetch_desc(lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.wk : &maps.wv);
     // Marks of the sequences named once and twice, in the ring before its first tile.
     uint32_t* once = reinterpret_cast<uint32_t*>(smem + L::kRing);
     uint32_t* twice = once + kPagedMaxSeqs / 32;

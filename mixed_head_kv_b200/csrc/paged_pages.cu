@@ -25,6 +25,11 @@ constexpr int kCopyChunk = kCopyThreads * kCopyUnroll * 16;    // bytes a CTA mo
 
 __device__ __forceinline__ int pages_of(int32_t len, int32_t P) { return (len + P - 1) / P; }
 
+// Pages an entry asks for, as a summand: what no pool has stays more than any pool
+// has, and 512 of them still fit 32 bits.
+constexpr int kTooMany = DUO_PAGED_MAX_PAGES + 1;
+__device__ __forceinline__ int summand(int pages) { return pages < kTooMany ? pages : kTooMany; }
+
 // A length the table can hold; anything else is treated as damaged.
 __device__ __forceinline__ bool len_ok(const PagedView& v, int32_t len) {
     return len >= 0 && static_cast<int64_t>(len) <= static_cast<int64_t>(v.max_pages) * v.P;
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan_kernel(const Page
         cow = v.ref[tail] - before > 1;
     }
     const int had = pages_of(len, v.P);
-    const int need = pages_of(len + add, v.P) - had + (cow ? 1 : 0);
+    const int need = summand(pages_of(len + add, v.P) - had + (cow ? 1 : 0));
     int total, n_cow;
     const int off = block_scan(need, sh.warp_sum, total);
     const int at = block_scan(cow ? 1 : 0, sh.warp_sum, n_cow);
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) copy_plan_kernel(const PageOp
             len = 0;
         }
     }
-    const int need = dst >= 0 ? pages_of(len, v.P) : 0;
+    const int need = dst >= 0 ? summand(pages_of(len, v.P)) : 0;
     int total;
     const int off = block_scan(need, sh.warp_sum, total);
     if (i < kPagedMaxBatch) {

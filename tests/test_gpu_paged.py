@@ -570,6 +570,19 @@ def test_pages_refusals(duo):
     assert c.error_flags() == A
 
 
+def test_pages_requests_beyond_any_pool(duo):
+    """Needs whose sum passes 32 bits are refused like any other that the pool cannot meet."""
+    c = make(duo, Hkv=1, G=1, D=64, P=16, num_pages=9, max_pages=1 << 23, max_seqs=512, mask=[0])
+    seqs = ints(range(512))
+    c.extend(seqs, ints([1 << 27] * 512))
+    assert c.error_flags() == duo.DUO_ERR_BIT_PAGED_CAPACITY
+    assert int(c.seq_len.abs().sum()) == 0 and int(c.page_ref.abs().sum()) == 0
+    c.extend(seqs, ints([(1 << 27) + 1] * 512))
+    assert c.error_flags() == duo.DUO_ERR_BIT_PAGED_CAPACITY
+    c.extend(ints([7]), ints([9 * 16]))
+    assert c.error_flags() == 0 and int(c.seq_len[7]) == 144
+
+
 @pytest.mark.parametrize("num_pages", [1, 3, 1023, 1025, 4097, 70001])
 def test_pages_pool_sizes(duo, num_pages):
     """The last page of a pool of any size is found, and no page behind it."""

@@ -110,7 +110,8 @@ def test_tensor_checks():
     for args in ((i32(0), q, k, k, out), (i32(0, 1), rows(2, 11), k, k, out), (i32(0, 1), q, rows(2, 4, 64), k, out),
                  (i32(0, 1), q.float(), k, k, out), (i32(0, 1), q, k, rows(2, 8)[:, ::2], out),
                  (i32(0, 1), q, k, rows(2, 8)[:, :4], out), (i32(0, 1), q, k, k, out[:1]),
-                 (i32(0, 1), q.transpose(0, 1).contiguous().transpose(0, 1), k, k, out)):
+                 (i32(0, 1), q.transpose(0, 1).contiguous().transpose(0, 1), k, k, out),
+                 (i32(0, 1), q[:1].expand(2, 12, 128), k, k, out), (i32(0, 1), q, k[:1].expand(2, 4, 128), k, out)):
         with pytest.raises(ValueError):
             c.decode(0, *args)
     with pytest.raises(ValueError):

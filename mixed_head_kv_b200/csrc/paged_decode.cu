@@ -10,18 +10,22 @@
 // into equal shares:
 //   - a tile is 64 bf16 rows (128 rows of E4M3 codes) of K and V of one (entry,
 //     KV head); D = 64 tiles are half that. The tiles of all retrieval (entry,
-//     head) pairs, then of all streaming pairs, form one sequence of T tiles;
-//     CTA c of C takes tiles [T c / C, T (c + 1) / C). Ragged batches, one long
+//     head) pairs, then of all streaming pairs, form one list, and every pair has
+//     one unit more, for the work at its end, which takes about as long as a tile.
+//     CTA c takes the c-th equal share of the units. Ragged batches, one long
 //     sequence and many short ones balance alike, and the lengths are read on
 //     the device: a captured launch stays right as the sequences grow;
 //   - a pair cut by a share boundary is joined by the last of its CTAs to
 //     finish: each leaves its unnormalised sums, maximum and weight in the
-//     workspace, at most two per CTA. The joining order is the CTA order, so
-//     results do not depend on which CTA is last.
+//     workspace, at most two per CTA, and counts itself once all its tiles are
+//     done (counting and joining between tiles cost 2 to 6 us of streaming each).
+//     The joining order is the CTA order, so results do not depend on which CTA
+//     is last.
 // Two CTAs per SM: 4 warps compute, 1 warp loads.
-//   - the loading warp streams tiles through a ring of 96 KB by TMA (page-sized
-//     boxes, 128-byte swizzle; page numbers are fetched 32 at a time, one load
-//     ahead) and the group's queries and the new rows through a 2-slot ring;
+//   - the loading warp finds the pairs of the share, publishes each through a
+//     2-slot ring together with the group's queries and the new rows, and streams
+//     tiles through a ring of 96 KB by TMA (boxes of page or tile size, 128-byte
+//     swizzle; page numbers are fetched 32 at a time);
 //   - every computing warp owns 16 (32) rows of each tile and runs on its own: no
 //     barrier inside a pair. S^T = K Q^T and O^T = V^T P^T with m16n8k16: the
 //     rows are the M side, so the group's heads fill the N side up to 8 and the
@@ -33,7 +37,14 @@
 //   - softmax in the exp2 domain, 32-bit statistics and sums; the maximum is
 //     moved only when a score exceeds it by more than 2^8 (exact: all terms stay
 //     relative to the same maximum). P is rounded to bf16 (f16 with E4M3): the
-//     operand type, relative error 2^-9 (2^-12) per term.
+//     operand type, relative error at most 2^-8 (2^-11) per term.
+// Measured (captured launches): 4 x 131072 tokens, groups of 4, half of 8 KV heads
+// retrieval: 164 us, 6.56 TB/s, the copy rate. 32769 tokens, 8 of 32 heads
+// retrieval: 30 us, 4.6 TB/s; 48 ragged sequences of E4M3 codes 24 us; 200 of
+// groups of 8 27 us; 529 tokens 7.8 us. What the smaller ones take beyond the
+// bytes is fixed: about 3 us until the first tiles arrive (lengths, the sums over
+// the entries, page numbers, rows: a chain of loads), 2 us at each pair's end and
+// 4 us for counting and joining.
 // Rows behind the last one in a page hold anything: their scores are replaced,
 // and their V rows are zeroed in shared memory (0 x NaN would not be 0).
 #include "paged_internal.cuh"

@@ -23,26 +23,32 @@
 // Warp roles (384 threads; registers moved from the last group to the others):
 //   warps 0-3  softmax of tile A, one thread per row    warps 4-7  of tile B
 //   warp 8     takes the items, loads Q, the K and the V tiles (2 stages each)
-//   warp 9     issues the products (the whole warp runs the loop, one lane issues:
-//              a loop that one lane runs alone issued them at half the rate), owns TMEM
+//   warp 9     issues the products (the whole warp runs the loop, one lane issues),
+//              owns TMEM
 //   warps 10-11 clear the V tiles that are seen in part of what a weight of zero
 //              must not meet
 // TMEM (512 columns): S of A and B, 128 columns each, P (bf16) written over the S
 // it was made from, O of A and of B at 256.
-// Softmax in the exp2 domain; the running maximum moves only when it grows by
-// more than 2^8 (exact), sums in 32 bits; P rounded to bf16, the operand type
+// Softmax in the exp2 domain; the running maximum moves only when a score exceeds it by
+// more than 2^8, or 64 weights add up to more than 2^10 (exact: all terms stay
+// relative to the same maximum), sums in 32 bits; P rounded to bf16, the operand type
 // (relative 2^-8 at most per term). Every mbarrier wait is bounded; on timeout the
 // CTA records kErrPagedWait and unwinds.
 //
-// Measured: 32768 rows, D = 128: 8 retrieval heads 1.80 ms, 1220 TFLOP/s; 24
-// streaming heads (sink 64, recent 256) 0.30 ms, 430 TFLOP/s of unmasked pairs, of
+// Measured: 32768 rows, D = 128: 8 retrieval heads 1.65 ms, 1330 TFLOP/s; 24
+// streaming heads (sink 64, recent 256) 0.26 ms, 490 TFLOP/s of unmasked pairs, of
 // which a 128 x 128 tile holds about half. 12 prompts of 40 to 2500 rows, 16 query
-// heads on retrieval KV heads 78 us; 160 prompts of up to 150 rows 25 us; one of 37
-// rows 7.7 us, a chain of launch, plan, loads, two products and the output. Two
-// threads per row in 16 softmax warps (512 + 128 threads), four per row in the
-// layout of 16-lane TMEM accesses, and output warps of their own all measured 3 to
-// 10 % slower on the retrieval heads; a polynomial for part of the exponentials
-// gained 1 % at most.
+// heads on retrieval KV heads 72 us; 160 prompts of up to 150 rows 22 us; one of 37
+// rows 7.7 us, a chain of launch, plan, loads, two products and the output.
+// A pair of tiles takes about 3500 cycles per 128 keys, where either pipe needs 2048.
+// What is left is the chain of one tile (scores out of TMEM 300, weights 1950 with the
+// other tile on the same unit half of the time, handing over, 768 of products, 130
+// until the scores are seen) and the issuing warp, which cannot run ahead of the
+// tensor core and stands still between two products at each of its three waits.
+// Slower by 3 to 20 %: two or four threads per row in 16 softmax warps, output warps
+// of their own, an issuing warp per tile (the tiles then run in step instead of in
+// turn), all waits before one run of products; a polynomial for part of the
+// exponentials gained 1 % at most.
 #include <type_traits>
 
 #include "paged_internal.cuh"
@@ -56,6 +62,11 @@ constexpr int kPackThreads = 384;
 constexpr int kSoftmaxRegs = 216;
 constexpr int kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers of a 384-thread launch");
+
+// A row's 64 weights against the maximum so far may add up to this much; with more,
+// the maximum moves. (64 weights of 1 for a row of equal scores, 16 times that for
+// scores that grow; far from what 32 bits cannot hold.)
+constexpr float kMaxHalfSum = 1024.f;
 
 // One work item, as the roles read it from the queue.
 struct PackItem {
@@ -117,6 +128,7 @@ constexpr int kOEmpty = 19;   // + tile, O read out (4 arrivals)
 constexpr int kItemFull = 21;   // + slot
 constexpr int kItemEmpty = 25;  // + slot
 constexpr int kDrain = 29;
+constexpr int kHalfDone = 32;  // + tile, one phase per first half of a product PV
 constexpr int kQueueSlots = 4;
 constexpr int kConsumers = 11;  // 8 softmax warps, the issuer, 2 V warps
 
@@ -188,50 +200,48 @@ __device__ __forceinline__ uint32_t elect_lane() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r;
 }
-// Products issued by the lanes with `lead` set only, several in one piece of assembly:
-// the issuing warp has 64 cycles per product, and a predicate or an address made anew
-// for each would cost a third of them. Descriptors advance by the operand's bytes / 16.
+// Several products in one piece of assembly, issued by one lane: the issuing warp has 64
+// cycles per product. Descriptors advance by the operand's bytes / 16.
 //
 // D[tmem] = A[smem] * B[smem]^T over four steps of 16 (one 64-column block).
-__device__ __forceinline__ void tc_mma_ss4_by(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ss4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-        "setp.ne.b32 e, %5, 0;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.eq.b32 q, 0, 0;\n\t"
         "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
         "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem] over four steps of 16 rows of B.
-__device__ __forceinline__ void tc_mma_ts4_by(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem] over four steps of 16 (64 rows of V).
+__device__ __forceinline__ void tc_mma_ts4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
-        "setp.ne.b32 e, %5, 0;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.eq.b32 q, 0, 0;\n\t"
         "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
         "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void tc_commit_by(uint32_t lead, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-        "r"(lead)
-        : "memory");
+
+// An arrival without a branch around it, which would end the block that the compiler
+// schedules.
+__device__ __forceinline__ void mbar_arrive_if(bool yes, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"(static_cast<uint32_t>(yes))
+                 : "memory");
 }
 
 template <int N>
@@ -462,6 +472,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             mbar_init(bar(kVEmpty + s), 1);
             mbar_init(bar(kSFull + s), 1);
             mbar_init(bar(kODone + s), 1);
+            mbar_init(bar(kHalfDone + s), 1);
             mbar_init(bar(kOEmpty + s), 4);
             mbar_init(bar(kPFull + 2 * s), 4);
             mbar_init(bar(kPFull + 2 * s + 1), 4);
@@ -721,15 +732,16 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 if (wait && !__all_sync(0xffffffffu, mbar_wait_compact(bar(kKFull + st), (t >> 1) & 1, abort_flag))) return false;
                 tc_fence_after();
                 const uint64_t q = dq + x * (Lay::kTile >> 4), k = dk + st * (Lay::kTile >> 4);
+                if (lead) {
 #pragma unroll
-                for (int kb = 0; kb < D / 64; ++kb)
-                    tc_mma_ss4_by(lead, tmem + x * kTileK, q + kb * (kTileBytesPerColBlock >> 4),
-                                  k + kb * (kTileBytesPerColBlock >> 4), idesc_qk, kb);
-                tc_commit_by(lead, bar(kSFull + x));
-                if (last) {
-                    tc_commit_by(lead, bar(kKEmpty + st));
-                    if (last_q) tc_commit_by(lead, bar(kQEmpty));
+                    for (int kb = 0; kb < D / 64; ++kb)
+                        tc_mma_ss4(tmem + x * kTileK, q + kb * (kTileBytesPerColBlock >> 4),
+                                   k + kb * (kTileBytesPerColBlock >> 4), idesc_qk, kb);
+                    tc_commit(bar(kSFull + x));
+                    if (last) tc_commit(bar(kKEmpty + st));
+                    if (last && last_q) tc_commit(bar(kQEmpty));
                 }
+                __syncwarp();
                 return true;
             };
             // O(x) += P(x) V(t); `first`: of the item.
@@ -745,11 +757,15 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 for (int half = 0; half < 2; ++half) {
                     if (!__all_sync(0xffffffffu, mbar_wait_compact(bar(kPFull + 2 * x + half), count & 1, abort_flag))) return false;
                     tc_fence_after();
-                    tc_mma_ts4_by(lead, tmem + kTmemO + x * 128, tmem + x * kTileK + half * 32, vt + half * 4 * (2048 >> 4),
-                                  idesc_pv, first && half == 0 ? 0u : 1u);
+                    if (lead) {
+                        tc_mma_ts4(tmem + kTmemO + x * 128, tmem + x * kTileK + half * 32, vt + half * 4 * (2048 >> 4), idesc_pv,
+                                   first && half == 0 ? 0u : 1u);
+                        if (half == 0) tc_commit(bar(kHalfDone + x));
+                        if (half == 1) tc_commit(bar(kODone + x));
+                        if (half == 1 && last) tc_commit(bar(kVEmpty + st));
+                    }
+                    __syncwarp();
                 }
-                tc_commit_by(lead, bar(kODone + x));
-                if (last) tc_commit_by(lead, bar(kVEmpty + st));
                 return true;
             };
             constexpr std::integral_constant<int, 0> A{};
@@ -798,7 +814,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 n = next_n;
             }
             if (!ok && lead) give_up(p.err, abort_flag);
-            tc_commit_by(lead, bar(kDrain));  // every product issued has completed before TMEM is released
+            if (lead) tc_commit(bar(kDrain));  // every product issued has completed before TMEM is released
             mbar_wait_compact(bar(kDrain), 0, nullptr);
         }
         __syncwarp();
@@ -827,7 +843,11 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             const bool single = it.p1 - it.p0 == 1;
             const RowKeys keys = row_keys(p, it, pr.row, q0 + row);
             auto seen_bits = [&](int k0) { return keys.bits(k0); };
+            // The first key tiles, which all rows of the warp see whole (a streaming item's few
+            // tiles are looked at one by one).
+            const int whole_tiles = single && it.retr ? (q0 + quarter * 32 + 1) / kTileK : 0;
             float m_run = -INFINITY, l_run = 0.f;
+            bool settled = false;  // every row of the warp has a maximum
             for (int j = 0; j < n; ++j, ++count) {
                 if (!__all_sync(0xffffffffu, mbar_wait(bar(kSFull + x), count & 1, abort_flag))) {
                     ok = false;
@@ -839,8 +859,8 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 // of each is all of it, nothing, or a part: one bit per run, the same for the
                 // whole warp. Only parts are masked element by element; a run that no row sees
                 // costs nothing but a zero P.
-                uint32_t none, all;
-                {
+                uint32_t none = 0u, all = 15u;
+                if (j >= whole_tiles) {
                     auto below = [](int x) { return (1u << (x < 0 ? 0 : x > 4 ? 4 : x)) - 1u; };
                     const int d = (q0 + quarter * 32 - row0) >> 5;  // the diagonal's run
                     none = ~below(d + 1);
@@ -854,28 +874,91 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                     all = __shfl_sync(0xffffffffu, all, 0);
                     none = __shfl_sync(0xffffffffu, none, 0);
                 }
-                // Two versions of what follows. A tile seen whole is handled at once, unrolled
-                // over its 128 columns. Any other is handled run by run, each run read from
-                // TMEM twice (for the maximum, for the weights), which costs next to nothing,
-                // and in a quarter of the code: the roles' loops have to fit the instruction
-                // cache together.
-                const bool whole = all == 15u;
-                uint32_t s[4][32];
-                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto max_of = [&](const uint32_t (&run)[32]) {
+                // Two versions of what follows.
+                //
+                // A tile seen whole, once every row of the warp has a maximum, is taken at that
+                // maximum at once, in halves of 64 keys, unrolled: a half's sum of weights shows
+                // whether a score outgrew it. Looking for the maximum first took a quarter of
+                // the time from the scores to their weights, a chain that the other tile's work
+                // does not hide.
+                //
+                // Any other tile, and a half whose sum is too large (or NaN), is handled run by
+                // run, each run read from TMEM twice (for the maximum, for the weights), in a
+                // quarter of the code: the roles' loops have to fit the instruction cache
+                // together. Weights go over S columns that have been read (run c's over 16 c ..)
+                // and only when no second look at S can be needed.
+                auto exps_of = [&](uint32_t (&run)[32], uint64_t negm) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], __uint_as_float(run[i]), __uint_as_float(run[i + 1]));
+                    for (int i = 0; i < 32; i += 2) {
+                        float e0, e1;
+                        f2unpack(ffma2(f2pack(__uint_as_float(run[i]), __uint_as_float(run[i + 1])), scale2, negm), e0, e1);
+                        run[i] = __float_as_uint(fast_exp2(e0));
+                        run[i + 1] = __float_as_uint(fast_exp2(e1));
+                    }
                 };
-                if (whole) {
+                auto pack_weights = [&](const uint32_t (&run)[32], uint32_t (&pk)[16], uint64_t (&acc)[2]) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+                    for (int i = 0; i < 32; i += 2) {
+                        const float p0 = __uint_as_float(run[i]), p1 = __uint_as_float(run[i + 1]);
+                        acc[(i >> 1) & 1] = fadd2(acc[(i >> 1) & 1], f2pack(p0, p1));
+                        pk[i >> 1] = pack_bf16x2(p0, p1);
+                    }
+                };
+                auto sum_of = [&](const uint64_t (&acc)[2]) {
+                    float a0, a1;
+                    f2unpack(fadd2(acc[0], acc[1]), a0, a1);
+                    return a0 + a1;
+                };
+                auto hand_over = [&](int half) {  // 64 keys' weights are written
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_if(lane == 0, bar(kPFull + 2 * x + half));
+                };
+                int c_slow = 0;  // runs from here on are handled one by one
+                if (all == 15u && settled) {
+                    uint32_t s[4][32], pk[2][16];
+                    uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+                    const uint64_t negm = f2pack(-m_run, -m_run);
+                    tmem_ld32(tS, s[0]);
+                    tmem_ld32(tS + 32, s[1]);
                     tc_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) max_of(s[c]);
-                } else {
+                    tmem_ld32(tS + 64, s[2]);
+                    tmem_ld32(tS + 96, s[3]);
+                    // The exponentials of a run are on their way while the run before is summed
+                    // and packed: with both in one loop a warp on its own took 455 cycles per
+                    // run, of which its exponentials need 256.
+                    exps_of(s[0], negm);
+                    exps_of(s[1], negm);
+                    pack_weights(s[0], pk[0], acc);
+                    tc_wait_ld();
+                    exps_of(s[2], negm);
+                    pack_weights(s[1], pk[1], acc);
+                    float sum = sum_of(acc);
+                    if (__all_sync(0xffffffffu, sum <= kMaxHalfSum)) {
+                        tmem_st16(tS, pk[0]);
+                        tmem_st16(tS + 16, pk[1]);
+                        l_run += sum;
+                        acc[0] = acc[1] = f2pack(0.f, 0.f);
+                        exps_of(s[3], negm);
+                        hand_over(0);
+                        pack_weights(s[2], pk[0], acc);
+                        pack_weights(s[3], pk[1], acc);
+                        sum = sum_of(acc);
+                        c_slow = 2;
+                        if (__all_sync(0xffffffffu, sum <= kMaxHalfSum)) {
+                            tmem_st16(tS + 32, pk[0]);
+                            tmem_st16(tS + 48, pk[1]);
+                            l_run += sum;
+                            hand_over(1);
+                            c_slow = 4;
+                        }
+                    }
+                }
+                if (c_slow < 4) {
+                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = c_slow; c < 4; ++c) {
                         if ((none >> c) & 1u) continue;
                         uint32_t run[32];
                         tmem_ld32(tS + c * 32, run);
@@ -887,81 +970,61 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                                 if (!((bits >> k) & 1u)) run[k] = 0xFF800000u;  // -inf
                             tmem_st32(tS + c * 32, run);  // for the second pass
                         }
-                        max_of(run);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], __uint_as_float(run[i]), __uint_as_float(run[i + 1]));
                     }
                     tc_wait_st();
-                }
-                const float mt = fmax3(fmaxf(m[0], m[1]), m[2], m[3]) * p.scale_log2;
-                float factor = 1.f;
-                if (mt > m_run + kRescaleThreshold) {
-                    factor = fast_exp2(m_run - mt);
-                    m_run = mt;
-                }
-                // PV(j-1) is the last product that wrote O.
-                if (j >= 1 && __any_sync(0xffffffffu, factor != 1.f)) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone + x), (count - 1) & 1, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                    const float mt = fmax3(fmaxf(m[0], m[1]), m[2], m[3]) * p.scale_log2;
+                    if (__any_sync(0xffffffffu, mt > m_run + kRescaleThreshold)) {
+                        float factor = 1.f;
+                        if (mt > m_run + kRescaleThreshold) {
+                            factor = fast_exp2(m_run - mt);
+                            m_run = mt;
+                        }
+                        l_run *= factor;
+                        settled = __all_sync(0xffffffffu, m_run > -INFINITY);
+                        if (j >= 1) {
+                            // The last product that wrote O: PV(j-1), or PV(j) of the half before.
+                            const bool ready = c_slow == 0 ? mbar_wait(bar(kODone + x), (count - 1) & 1, abort_flag)
+                                                           : mbar_wait(bar(kHalfDone + x), count & 1, abort_flag);
+                            if (!__all_sync(0xffffffffu, ready)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t r[16];
-                        tmem_ld16(tO + c * 16, r);
-                        tc_wait_ld();
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t r[16];
+                                tmem_ld16(tO + c * 16, r);
+                                tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * factor);
-                        tmem_st16(tO + c * 16, r);
+                                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * factor);
+                                tmem_st16(tO + c * 16, r);
+                            }
+                        }
                     }
-                }
-                const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                const uint64_t negm = f2pack(-m_use, -m_use);
-                uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-                // P of a run goes over S columns that have been read: 16 c .. of run c and before.
-                auto weights_of = [&](const uint32_t (&run)[32], int c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float e0, e1;
-                        f2unpack(ffma2(f2pack(__uint_as_float(run[i]), __uint_as_float(run[i + 1])), scale2, negm), e0, e1);
-                        const float p0 = fast_exp2(e0), p1 = fast_exp2(e1);
-                        acc[(i >> 1) & 1] = fadd2(acc[(i >> 1) & 1], f2pack(p0, p1));
-                        pk[i >> 1] = pack_bf16x2(p0, p1);
-                    }
-                    tmem_st16(tS + c * 16, pk);
-                };
-                auto hand_over = [&](int half) {  // 64 keys' weights are written
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kPFull + 2 * x + half));
-                };
-                if (whole) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        weights_of(s[c], c);
-                        if (c & 1) hand_over(c >> 1);
-                    }
-                } else {
+                    const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                    const uint64_t negm = f2pack(-m_use, -m_use);
+                    uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = c_slow; c < 4; ++c) {
+                        uint32_t pk[16];
                         if ((none >> c) & 1u) {
-                            uint32_t zero[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) zero[i] = 0u;
-                            tmem_st16(tS + c * 16, zero);
+                            for (int i = 0; i < 16; ++i) pk[i] = 0u;
                         } else {
                             uint32_t run[32];
                             tmem_ld32(tS + c * 32, run);
                             tc_wait_ld();
-                            weights_of(run, c);
+                            exps_of(run, negm);
+                            pack_weights(run, pk, acc);
                         }
+                        tmem_st16(tS + c * 16, pk);
                         if (c & 1) hand_over(c >> 1);
                     }
+                    l_run += sum_of(acc);
                 }
-                float a0, a1;
-                f2unpack(fadd2(acc[0], acc[1]), a0, a1);
-                l_run = l_run * factor + (a0 + a1);
             }
             if (!ok) break;
             if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone + x), (count - 1) & 1, abort_flag))) {

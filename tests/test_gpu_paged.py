@@ -394,6 +394,28 @@ def test_prefill_poisoned_neighbour_and_large_scores(duo):
     check_prompts(c, 0, [0, start[1]], q, k, v64, out)
 
 
+@pytest.mark.parametrize("G,D", [(1, 128), (2, 128), (2, 64)])
+def test_prefill_maxima_that_move_late(duo, G, D):
+    """Scores whose maximum moves in the middle of a prompt, in either half of a key tile, by a little, by 2^30 and by
+    more than 32 bits hold, up and down, for some rows of a tile and not for others. Keys are constant rows of few
+    bits, so every score is exact up to the scale's rounding, whatever its size."""
+    c = make(duo, Hkv=2, G=G, D=D, S=70, R=900, mask=[1, 0])
+    n = 1300
+    start, (q, k, v) = packed([n], 2 * G, 2, D, seed=40 + G)
+    level = torch.zeros(n)
+    for at, to in ((300, 0.25), (330, 0.5), (460, 2.5), (500, 2.0), (650, 4.5), (718, 5.0), (719, 15.0), (730, 6.0), (1100, 1.0),
+                   (1170, 15.5)):
+        level[at:] = to
+    level += torch.randint(0, 6, (n,), generator=torch.Generator().manual_seed(3)) / 16
+    k[:] = level.to(k).view(n, 1, 1)
+    sign = torch.tensor([1.0, -1.0, 0.5, 1.0, 0.0])[torch.arange(n) % 5]
+    q[:] = sign.to(q).view(n, 1, 1)
+    out = torch.full_like(q, float("nan"))
+    c.prefill(0, ints(start), q, k, v, out)
+    check_prompts(c, 0, start, q, k, v, out)
+    assert c.error_flags() == 0
+
+
 @pytest.mark.parametrize("G", [1, 2])
 @pytest.mark.parametrize("S,R", [(4, 40), (130, 300)])
 def test_prefill_non_finite_values_reach_their_readers_only(duo, G, S, R):

@@ -523,8 +523,15 @@ class PagedCache:
         import torch
         self._int32, self._bf16 = torch.int32, torch.bfloat16
         self._index = -1 if self.device.type == "cpu" else self.device.index
+        self._raw_stream = None if self.device.type == "cpu" else getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._dim, self._q_heads, self._kv_heads = (self.layout.head_dim, self.layout.num_q_heads,
                                                     self.layout.num_kv_heads)
+
+    def _on(self, stream):
+        """The stream's handle; by default the current one of the cache's device."""
+        if stream is None and self._raw_stream is not None:
+            return self._raw_stream(self._index)
+        return _stream(stream)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -548,13 +555,14 @@ class PagedCache:
     def _rows(self, name, t, heads, n=None):
         """(address, row stride) of packed rows [n, heads, head_dim]."""
         d = self._dim
-        shape = t.shape
-        if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype is not self._bf16 or t.get_device() != self._index:
+        rows, h, w = t.shape if t.dim() == 3 else (0, -1, -1)
+        if h != heads or w != d or t.dtype is not self._bf16 or t.get_device() != self._index:
             raise ValueError(f"{name}: expected bfloat16 rows [*, {heads}, {d}] on {self.device}, got {t.dtype} "
-                             f"{tuple(shape)} on {t.device}")
-        rows = shape[0]
+                             f"{tuple(t.shape)} on {t.device}")
         if n is not None and rows != n:
             raise ValueError(f"{name}: expected {n} rows, got {rows}")
+        if t.is_contiguous():
+            return t.data_ptr(), 0
         s = t.stride()
         if rows and (s[2] != 1 or (heads > 1 and s[1] != d) or (rows > 1 and s[0] < heads * d)):
             raise ValueError(f"{name}: rows must be dense and must not overlap, got strides {s}")
@@ -579,7 +587,7 @@ class PagedCache:
         a = self._entries("seqs", seqs)
         n = seqs.shape[0]
         b = None if n_tok is None else self._entries("n_tok", n_tok, n)
-        _check(_lib.duo_paged_extend(self.handle, n, a, b, _stream(stream)), "duo_paged_extend")
+        _check(_lib.duo_paged_extend(self.handle, n, a, b, self._on(stream)), "duo_paged_extend")
 
     def append(self, layer, seqs, row_start, k, v, stream=None):
         """Rows [row_start[i], row_start[i + 1]) of k and v are the newest tokens of seqs[i]."""
@@ -588,7 +596,7 @@ class PagedCache:
         b = self._entries("row_start", row_start, n + 1)
         rows = k.shape[0]
         kp, vp, ks = self._kv(k, v, rows)
-        _check(_lib.duo_paged_append(self.handle, layer, n, a, b, kp, vp, rows, ks, _stream(stream)), "duo_paged_append")
+        _check(_lib.duo_paged_append(self.handle, layer, n, a, b, kp, vp, rows, ks, self._on(stream)), "duo_paged_append")
 
     def prefill(self, layer, row_start, q, k, v, out, stream=None):
         """Whole prompts: rows [row_start[i], row_start[i + 1]) of q, k, v and out."""
@@ -600,7 +608,7 @@ class PagedCache:
         qp, qs = self._rows("q", q, heads)
         kp, vp, ks = self._kv(k, v, rows)
         op, os_ = self._rows("out", out, heads, rows)
-        _check(_lib.duo_paged_prefill(self.handle, layer, n, b, qp, kp, vp, op, rows, qs, ks, os_, _stream(stream)),
+        _check(_lib.duo_paged_prefill(self.handle, layer, n, b, qp, kp, vp, op, rows, qs, ks, os_, self._on(stream)),
                "duo_paged_prefill")
 
     def decode(self, layer, seqs, q, k_new, v_new, out, stream=None):
@@ -610,7 +618,7 @@ class PagedCache:
         qp, qs = self._rows("q", q, heads, n)
         kp, vp, ks = self._kv(k_new, v_new, n)
         op, os_ = self._rows("out", out, heads, n)
-        _check(_lib.duo_paged_decode(self.handle, layer, n, a, qp, kp, vp, op, qs, ks, os_, _stream(stream)),
+        _check(_lib.duo_paged_decode(self.handle, layer, n, a, qp, kp, vp, op, qs, ks, os_, self._on(stream)),
                "duo_paged_decode")
 
     def _pairs(self, src, dst):
@@ -620,19 +628,19 @@ class PagedCache:
     def fork(self, src, dst, stream=None):
         """Empty sequence dst[i] shares the pages of src[i]."""
         n, a, b = self._pairs(src, dst)
-        _check(_lib.duo_paged_fork(self.handle, n, a, b, _stream(stream)), "duo_paged_fork")
+        _check(_lib.duo_paged_fork(self.handle, n, a, b, self._on(stream)), "duo_paged_fork")
 
     def copy(self, src, dst, stream=None):
         """Empty sequence dst[i] becomes a copy of src[i] in pages of its own."""
         n, a, b = self._pairs(src, dst)
-        _check(_lib.duo_paged_copy(self.handle, n, a, b, _stream(stream)), "duo_paged_copy")
+        _check(_lib.duo_paged_copy(self.handle, n, a, b, self._on(stream)), "duo_paged_copy")
 
     def release(self, seqs, stream=None):
         a = self._entries("seqs", seqs)
-        _check(_lib.duo_paged_release(self.handle, seqs.shape[0], a, _stream(stream)), "duo_paged_release")
+        _check(_lib.duo_paged_release(self.handle, seqs.shape[0], a, self._on(stream)), "duo_paged_release")
 
     def compact(self, stream=None):
-        _check(_lib.duo_paged_compact(self.handle, _stream(stream)), "duo_paged_compact")
+        _check(_lib.duo_paged_compact(self.handle, self._on(stream)), "duo_paged_compact")
 
     def error_flags(self, stream=None) -> int:
         st, f = duo_paged_error(self.handle, stream)

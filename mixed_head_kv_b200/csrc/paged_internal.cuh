@@ -52,6 +52,7 @@ struct PagePlan {           // what a planning kernel leaves for the copy kernel
     int32_t used;           // compact: pages in use (0: leave the table alone)
     int32_t pad;
     int2 seq[kPagedMaxBatch];  // (src, dst) windows
+    uint32_t arrived[kPagedMaxBatch];  // fork: CTAs of the entry that have looked at it; 0 between calls
 };
 struct PageOps {
     PagedView v;

@@ -11,10 +11,12 @@
 //   - the copy kernel moves the pages and windows that the plan lists, all heads
 //     of all layers. It is bound by HBM, read plus write, when there is
 //     something to copy, and a bare launch otherwise.
+// Fork and release need no plan and are one launch each.
 // Measured: forking 16 sequences into 64, extending those and releasing them (3.2 GB
-// of windows and last pages read and written) 0.54 ms, 6.0 TB/s; copying 12
-// sequences, releasing the originals and compacting (5.5 GB) 0.93 ms, 5.9 TB/s, of
-// a copy rate of 6.57; with nothing to copy 3 to 5 us per call.
+// of windows and last pages, the sources' counted for every fork) 0.47 ms, 6.8 TB/s;
+// copying 12 sequences, releasing the originals and compacting (5.5 GB) 0.93 ms, 5.9
+// TB/s, of a copy rate of 6.57; with nothing to copy 1 to 2 us for fork and release, 5
+// for the others.
 #include "paged_internal.cuh"
 #include "sm100.cuh"
 
@@ -342,28 +344,42 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(const Pag
     grid_launch_dependents();
 }
 
-constexpr int kEntryThreads = 128;
-
-// Fork (duo_paged_fork), one CTA per entry: the table row, the counts, the length.
-__global__ void __launch_bounds__(kEntryThreads) fork_kernel(const PageOps p) {
-    grid_dependency_wait();
-    const PagedView& v = p.v;
-    const int e = blockIdx.x;
-    const int src = p.a[e], dst = p.b[e];
-    bool bad = src < 0 || src >= v.max_seqs || dst < 0 || dst >= v.max_seqs;
-    const bool pad = bad;
-    if (!bad) {
-        // Refused without reading what another CTA may be writing: an entry whose
-        // dst stands elsewhere in the call. The others are the only writers of
-        // their dst, and no dst is a src.
-        bool hit = false;
-        for (int j = threadIdx.x; j < p.n; j += kEntryThreads) {
-            const int sj = p.a[j], dj = p.b[j];
-            if (sj < 0 || sj >= v.max_seqs || dj < 0 || dj >= v.max_seqs) continue;  // padding
-            hit |= sj == dst || (j != e && dj == dst);
-        }
-        bad = __syncthreads_or(hit) != 0;
+// Copies `bytes` (a multiple of 16) at from + at .. of one chunk.
+__device__ __forceinline__ void copy_chunk(const uint8_t* from, uint8_t* to, int64_t at, int64_t bytes) {
+    uint4 x[kCopyUnroll];
+#pragma unroll
+    for (int j = 0; j < kCopyUnroll; ++j) {
+        const int64_t o = at + j * (kCopyThreads * 16);
+        if (o < bytes) x[j] = ld_nc_v4(from + o);
     }
+#pragma unroll
+    for (int j = 0; j < kCopyUnroll; ++j) {
+        const int64_t o = at + j * (kCopyThreads * 16);
+        if (o < bytes) *reinterpret_cast<uint4*>(to + o) = x[j];
+    }
+}
+
+// Fork (duo_paged_fork), some CTAs per entry: its table row, the counts, the windows.
+// All of them look at the entry; the last to have done so writes the length, which
+// the others' checks read. (With the windows in a launch of their own, as the
+// other calls have it, a small fork took two latencies instead of one.)
+__global__ void __launch_bounds__(kCopyThreads) fork_kernel(const PageOps p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const PagedView& v = p.v;
+    const int e = blockIdx.y;
+    const int src = p.a[e], dst = p.b[e];
+    if (src < 0 || src >= v.max_seqs || dst < 0 || dst >= v.max_seqs) return;  // padding
+    // Refused without reading what another entry may be writing: an entry whose
+    // dst stands elsewhere in the call. The others are the only writers of
+    // their dst, and no dst is a src.
+    bool hit = false;
+    for (int j = threadIdx.x; j < p.n; j += kCopyThreads) {
+        const int sj = p.a[j], dj = p.b[j];
+        if (sj < 0 || sj >= v.max_seqs || dj < 0 || dj >= v.max_seqs) continue;  // padding
+        hit |= sj == dst || (j != e && dj == dst);
+    }
+    bool bad = __syncthreads_or(hit) != 0;
     int len = 0;
     if (!bad) {
         len = v.seq_len[src];
@@ -371,26 +387,30 @@ __global__ void __launch_bounds__(kEntryThreads) fork_kernel(const PageOps p) {
     }
     __syncthreads();  // every thread has read the lengths
     if (threadIdx.x == 0) {
-        p.plan->seq[e] = make_int2(bad ? -1 : src, dst);
-        if (bad && !pad) atomicOr(v.err, kErrPagedArgument);
-        if (!bad) v.seq_len[dst] = len;
-        if (e == 0) {
-            p.plan->n_pages = 0;
-            p.plan->n_seqs = p.n;
-            p.plan->used = 0;
+        __threadfence();
+        if (atomicAdd(&p.plan->arrived[e], 1u) == gridDim.x - 1) {
+            p.plan->arrived[e] = 0;
+            if (bad) atomicOr(v.err, kErrPagedArgument);
+            else v.seq_len[dst] = len;
         }
     }
-    if (!bad) {
-        const int n = pages_of(len, v.P);
-        for (int j = threadIdx.x; j < n; j += kEntryThreads) {
-            const int page = v.table[static_cast<int64_t>(src) * v.max_pages + j];
-            v.table[static_cast<int64_t>(dst) * v.max_pages + j] = page;
-            if (page >= 0 && page < v.num_pages) atomicAdd(&v.ref[page], 1);
-            else atomicOr(v.err, kErrPagedArgument);
-        }
+    if (bad) return;
+    const int n = pages_of(len, v.P);
+    for (int j = blockIdx.x * kCopyThreads + threadIdx.x; j < n; j += gridDim.x * kCopyThreads) {
+        const int page = v.table[static_cast<int64_t>(src) * v.max_pages + j];
+        v.table[static_cast<int64_t>(dst) * v.max_pages + j] = page;
+        if (page >= 0 && page < v.num_pages) atomicAdd(&v.ref[page], 1);
+        else atomicOr(v.err, kErrPagedArgument);
     }
-    grid_launch_dependents();
+    const int64_t bytes = static_cast<int64_t>(v.s_all) * v.W * v.D * 2;
+    const int64_t chunks = (bytes + kCopyChunk - 1) / kCopyChunk * 2;
+    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        uint8_t* base = reinterpret_cast<uint8_t*>((c & 1) ? v.v_window : v.k_window);
+        copy_chunk(base + src * bytes, base + dst * bytes, (c >> 1) * kCopyChunk + threadIdx.x * 16, bytes);
+    }
 }
+
+constexpr int kEntryThreads = 128;
 
 // Release (duo_paged_release), one CTA per entry.
 __global__ void __launch_bounds__(kEntryThreads) release_kernel(const PageOps p) {
@@ -447,17 +467,7 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PageOps 
         const int64_t at = (r >> 1) * kCopyChunk + threadIdx.x * 16;
         const uint8_t* from = base + m.x * bytes;
         uint8_t* to = base + m.y * bytes;
-        uint4 x[kCopyUnroll];
-#pragma unroll
-        for (int j = 0; j < kCopyUnroll; ++j) {
-            const int64_t o = at + j * (kCopyThreads * 16);
-            if (o < bytes) x[j] = ld_nc_v4(from + o);
-        }
-#pragma unroll
-        for (int j = 0; j < kCopyUnroll; ++j) {
-            const int64_t o = at + j * (kCopyThreads * 16);
-            if (o < bytes) *reinterpret_cast<uint4*>(to + o) = x[j];
-        }
+        copy_chunk(from, to, at, bytes);
     }
     if (used > 0) {
         for (int s = blockIdx.x; s < v.max_seqs; s += gridDim.x) {
@@ -499,8 +509,13 @@ cudaError_t launch_paged_extend(const PageOps& p, int num_sms, cudaStream_t s) {
     return e != cudaSuccess ? e : launch_copies(p, num_sms, s);
 }
 cudaError_t launch_paged_fork(const PageOps& p, int num_sms, cudaStream_t s) {
-    const cudaError_t e = launch_pdl(fork_kernel, dim3(static_cast<unsigned>(p.n)), dim3(kEntryThreads), 0, s, p);
-    return e != cudaSuccess ? e : launch_copies(p, num_sms, s);
+    // Six CTAs per SM over all entries, and no more than their windows' chunks.
+    const int64_t bytes = static_cast<int64_t>(p.v.s_all) * p.v.W * p.v.D * 2;
+    int64_t parts = (static_cast<int64_t>(num_sms) * 6 + p.n - 1) / p.n;
+    const int64_t chunks = (bytes + kCopyChunk - 1) / kCopyChunk * 2;
+    if (parts > chunks) parts = chunks;
+    if (parts < 1) parts = 1;
+    return launch_pdl(fork_kernel, dim3(static_cast<unsigned>(parts), static_cast<unsigned>(p.n)), dim3(kCopyThreads), 0, s, p);
 }
 cudaError_t launch_paged_copy(const PageOps& p, int num_sms, cudaStream_t s) {
     const cudaError_t e = launch_pdl(copy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);

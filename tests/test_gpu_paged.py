@@ -592,6 +592,30 @@ def test_pages_refusals(duo):
     assert c.error_flags() == A
 
 
+@pytest.mark.parametrize("S,R,n", [(44, 256, 6), (0, 2, 40), (300, 700, 1)])
+def test_fork_windows_of_many_chunks(duo, S, R, n):
+    """Windows larger than one CTA's piece, and smaller: every fork has its source's, bit for bit, a second call gives
+    what the first gave, and entries that are refused leave their sequence as it was."""
+    c = make(duo, Hkv=4, G=1, D=128, S=S, R=R, max_seqs=64, mask=[0, 1, 0, 0, 1, 1, 0, 0, 0, 0, 0, 0], layers=3)
+    for w in (c.k_window, c.v_window):
+        w.copy_(torch.randint(-100, 100, w.shape, generator=torch.Generator().manual_seed(S + R)).to(w))
+    c.extend(ints([0, 1, 2]), ints([37, 16, 5]))
+    before = [w.clone() for w in (c.k_window, c.v_window)]
+    for dst in (list(range(10, 10 + n)), list(range(63, 63 - min(n, 10), -1))):
+        src = [(i * i) % 3 for i in range(len(dst))]
+        # refused: a dst twice, a dst that is not empty, a dst that is a source; padding
+        c.fork(ints(src + [0, 1, 0, 2, -1, 0]), ints(dst + [5, 5, 1, 2, 9, 64]))
+        for w, b in zip((c.k_window, c.v_window), before):
+            for i, d in zip(src, dst):
+                b[d] = b[i]
+            assert torch.equal(w, b)
+        for i, d in zip(src, dst):
+            pages = -(-int(c.seq_len[i]) // 16)
+            assert c.seq_len[d] == c.seq_len[i] and torch.equal(c.page_table[d, :pages], c.page_table[i, :pages])
+        assert c.seq_len[5] == 0 and c.seq_len[9] == 0
+        assert c.error_flags() == duo.DUO_ERR_BIT_PAGED_ARGUMENT
+
+
 def test_pages_requests_beyond_any_pool(duo):
     """Needs whose sum passes 32 bits are refused like any other that the pool cannot meet."""
     c = make(duo, Hkv=1, G=1, D=64, P=16, num_pages=9, max_pages=1 << 23, max_seqs=512, mask=[0])

@@ -39,7 +39,7 @@
 // streaming heads (sink 64, recent 256) 0.26 ms, 490 TFLOP/s of unmasked pairs, of
 // which a 128 x 128 tile holds about half. 12 prompts of 40 to 2500 rows, 16 query
 // heads on retrieval KV heads 72 us; 160 prompts of up to 150 rows 22 us; one of 37
-// rows 7.7 us, a chain of launch, plan, loads, two products and the output.
+// rows 6.6 us, a chain of launch, plan, loads, two products and the output.
 // A pair of tiles takes about 3500 cycles per 128 keys, where either pipe needs 2048.
 // What is left is the chain of one tile (scores out of TMEM 300, weights 1950 with the
 // other tile on the same unit half of the time, handing over, 768 of products, 130
@@ -556,8 +556,8 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         regs_dec<kOtherRegs>();
         if (warp == 8 && lane == 0) {
             // -------------------------------------------------------- items, Q and K
-            // The next item is taken and published before this one's K tiles are loaded,
-            // so that nobody waits for the counter.
+            // The next item is taken and published behind the loads of this one's first key
+            // tile: nobody waits for the counter then, the first loads least of all.
             tma_prefetch_desc(&maps.q);
             int published = 0;
             auto publish = [&](PackItem& it) -> bool {
@@ -579,16 +579,9 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             int q_loads = 0, k_loads = 0;
             int raw0 = 0, raw1 = 0;   // V tiles that the V warps go through, by stage
             PackItem it, after;
-            it.idx = 0;
-            bool ok = true, first = true;
+            bool ok = publish(it);
             while (ok && it.idx >= 0) {
-                ok = publish(after);
-                if (first) {  // nothing to load yet
-                    first = false;
-                    it = after;
-                    continue;
-                }
-                if (ok && q_loads >= 1) ok = mbar_wait_compact(bar(kQEmpty), (q_loads - 1) & 1, abort_flag);
+                if (q_loads >= 1) ok = mbar_wait_compact(bar(kQEmpty), (q_loads - 1) & 1, abort_flag);
                 if (!ok) break;
                 mbar_arrive_expect_tx(bar(kQFull), (it.nb > 0 ? 2 : 1) * Lay::kTile);
 #pragma unroll 1
@@ -624,6 +617,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                                     it.start + row0);
                     if (part) ++(st ? raw1 : raw0);
                     else mbar_arrive(full);  // for the second of the V warps
+                    if (j == 0) ok = publish(after);
                 }
                 it = after;
             }

@@ -62,6 +62,9 @@ constexpr int kMaxG = DUO_PAGED_MAX_GROUP;
 // A pair is cut into at most about this many parts: joining reads G x D floats
 // of each part in one CTA.
 constexpr int kPartsPerPair = 48;
+// Units of work at the end of a pair. (48 and 200 ragged sequences: 24.3 and 27.2 us; with
+// 2 units 24.5 and 26.7, with 3 25.5 and 28.0.)
+constexpr int kEndUnits = 1;
 
 constexpr int kFull = 0;     // + stage (up to 6)
 constexpr int kEmpty = 6;    // + stage
@@ -203,7 +206,7 @@ struct Shares {
     }
 };
 
-// The list of work: units are the tiles of a pair and one more for its end (joining
+// The list of work: units are the tiles of a pair and kEndUnits for its end (joining
 // the warps and writing the result takes about as long as a tile), so that shares
 // of many short pairs weigh as much as shares of long ones.
 struct Work {
@@ -220,7 +223,7 @@ struct Work {
     __device__ __forceinline__ void fill(Segment& s, int n, int at, int64_t u, int64_t hi) const {
         const int64_t left = hi - u;
         const int end = left < n - at ? at + static_cast<int>(left) : n;
-        s.tiles = n - 1;
+        s.tiles = n - kEndUnits;
         s.units = end - at;
         s.t0 = at < s.tiles ? at : s.tiles;
         s.t1 = end < s.tiles ? end : s.tiles;
@@ -264,7 +267,7 @@ struct Work {
     // The one behind it, which starts at unit u: the next head, or the next entry
     // with rows, or the first of the windows.
     __device__ __forceinline__ void next(Segment& s, int64_t u, int64_t hi) const {
-        int units = s.tiles + 1;
+        int units = s.tiles + kEndUnits;
         ++s.idx;
         if (s.idx == (s.retr ? n_retr : n_retr + n_strm)) {
             if (u == of_retr) {
@@ -448,9 +451,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             len_of[i0 + j] = my_len[j];
             seq_of[i0 + j] = static_cast<uint16_t>(s < 0 ? 0 : s);
         }
-        if (my_len[j] > 0) {  // tiles, and one for the end of the pair
-            sum_r += (my_len[j] + kPageTile - 1) / kPageTile + 1;
-            sum_s += ((my_len[j] < v.W ? my_len[j] : v.W) + kWinTile - 1) / kWinTile + 1;
+        if (my_len[j] > 0) {  // tiles, and the end of the pair
+            sum_r += (my_len[j] + kPageTile - 1) / kPageTile + kEndUnits;
+            sum_s += ((my_len[j] < v.W ? my_len[j] : v.W) + kWinTile - 1) / kWinTile + kEndUnits;
         }
     }
     if (wrong && blockIdx.x == 0) report(v.err, kErrPagedArgument);

@@ -13,10 +13,10 @@
 //     something to copy, and a bare launch otherwise.
 // Fork and release need no plan and are one launch each.
 // Measured: forking 16 sequences into 64, extending those and releasing them (3.2 GB
-// of windows and last pages, the sources' counted for every fork) 0.47 ms, 6.8 TB/s;
-// copying 12 sequences, releasing the originals and compacting (5.5 GB) 0.93 ms, 5.9
-// TB/s, of a copy rate of 6.57; with nothing to copy 1 to 2 us for fork and release, 5
-// for the others.
+// of windows and last pages, the sources' counted for every fork, of which L2 serves
+// some) 0.36 ms, 8.9 TB/s; copying 12 sequences, releasing the originals and compacting
+// (5.5 GB) 0.85 ms, 6.5 TB/s, of a copy rate of 6.57; with nothing to copy 1 to 2 us
+// for release, 5 for the others.
 #include "paged_internal.cuh"
 #include "sm100.cuh"
 
@@ -26,6 +26,15 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kCopyThreads = 256;
+// CTAs per SM at most. About eight are resident, and a CTA's stores and its next loads do
+// not overlap: more CTAs than that, one behind the other, keep more in flight (copying
+// 12 sequences and compacting: 890 us with 8 for both, 850 with 64 and 8, 845 with 64
+// and 16; 16 forks into 64: 400 with 6, 360 with 24). Empty CTAs cost about 0.6 us per
+// eight and SM, so a call that often has nothing to copy has few.
+constexpr int kExtendCtas = 6;
+constexpr int kCompactCtas = 8;
+constexpr int kForkCtas = 24;
+constexpr int kCopyCtas = 64;
 constexpr int kCopyUnroll = 8;                                 // 16-byte loads in flight per thread
 constexpr int kCopyChunk = kCopyThreads * kCopyUnroll * 16;    // bytes a CTA moves at a time
 
@@ -355,7 +364,7 @@ __device__ __forceinline__ void copy_chunk(const uint8_t* from, uint8_t* to, int
 #pragma unroll
     for (int j = 0; j < kCopyUnroll; ++j) {
         const int64_t o = at + j * (kCopyThreads * 16);
-        if (o < bytes) *reinterpret_cast<uint4*>(to + o) = x[j];
+        if (o < bytes) __stcs(reinterpret_cast<uint4*>(to + o), x[j]);  // leaves L2 first: 474 -> 406 us for the forks
     }
 }
 
@@ -489,8 +498,19 @@ __global__ void unit_scales_kernel(float* dst, int n) {
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) dst[i] = 1.0f;
 }
 
-cudaError_t launch_copies(const PageOps& p, int num_sms, cudaStream_t s) {
-    return launch_pdl(paged_copy_kernel, dim3(static_cast<unsigned>(num_sms * 6)), dim3(kCopyThreads), 0, s, p);
+// `per_sm` CTAs per SM, and no more than there can be pieces: `pages` page pairs,
+// `windows` window pairs, the rows of the table.
+cudaError_t launch_copies(const PageOps& p, int num_sms, int64_t pages, int64_t windows, int64_t rows, int per_sm,
+                          cudaStream_t s) {
+    const PagedView& v = p.v;
+    const int64_t page_bytes = static_cast<int64_t>(v.r_all) * v.P * v.D * v.elem;
+    const int64_t win_bytes = static_cast<int64_t>(v.s_all) * v.W * v.D * 2;
+    int64_t grid = 2 * (pages * ((page_bytes + kCopyChunk - 1) / kCopyChunk) +
+                        windows * ((win_bytes + kCopyChunk - 1) / kCopyChunk));
+    if (grid < rows) grid = rows;
+    if (grid < 1) grid = 1;
+    if (grid > num_sms * per_sm) grid = num_sms * per_sm;
+    return launch_pdl(paged_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kCopyThreads), 0, s, p);
 }
 
 }  // namespace
@@ -506,12 +526,12 @@ cudaError_t launch_paged_unit_scales(float* dst, int n, cudaStream_t s) {
 
 cudaError_t launch_paged_extend(const PageOps& p, int num_sms, cudaStream_t s) {
     const cudaError_t e = launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
-    return e != cudaSuccess ? e : launch_copies(p, num_sms, s);
+    return e != cudaSuccess ? e : launch_copies(p, num_sms, p.n, 0, 0, kExtendCtas, s);
 }
 cudaError_t launch_paged_fork(const PageOps& p, int num_sms, cudaStream_t s) {
-    // Six CTAs per SM over all entries, and no more than their windows' chunks.
+    // Over all entries, and no more than their windows' chunks.
     const int64_t bytes = static_cast<int64_t>(p.v.s_all) * p.v.W * p.v.D * 2;
-    int64_t parts = (static_cast<int64_t>(num_sms) * 6 + p.n - 1) / p.n;
+    int64_t parts = (static_cast<int64_t>(num_sms) * kForkCtas + p.n - 1) / p.n;
     const int64_t chunks = (bytes + kCopyChunk - 1) / kCopyChunk * 2;
     if (parts > chunks) parts = chunks;
     if (parts < 1) parts = 1;
@@ -519,14 +539,14 @@ cudaError_t launch_paged_fork(const PageOps& p, int num_sms, cudaStream_t s) {
 }
 cudaError_t launch_paged_copy(const PageOps& p, int num_sms, cudaStream_t s) {
     const cudaError_t e = launch_pdl(copy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
-    return e != cudaSuccess ? e : launch_copies(p, num_sms, s);
+    return e != cudaSuccess ? e : launch_copies(p, num_sms, p.v.num_pages, p.n, 0, kCopyCtas, s);
 }
 cudaError_t launch_paged_release(const PageOps& p, cudaStream_t s) {
     return launch_pdl(release_kernel, dim3(static_cast<unsigned>(p.n)), dim3(kEntryThreads), 0, s, p);
 }
 cudaError_t launch_paged_compact(const PageOps& p, int num_sms, cudaStream_t s) {
     const cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
-    return e != cudaSuccess ? e : launch_copies(p, num_sms, s);
+    return e != cudaSuccess ? e : launch_copies(p, num_sms, p.v.num_pages / 2, 0, p.v.max_seqs, kCompactCtas, s);
 }
 
 }  // namespace duo

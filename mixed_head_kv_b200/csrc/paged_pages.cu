@@ -26,11 +26,12 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kCopyThreads = 256;
-// CTAs per SM at most. About eight are resident, and a CTA's stores and its next loads do
-// not overlap: more CTAs than that, one behind the other, keep more in flight (copying
+// CTAs per SM at most. Three or four are resident, and a CTA's stores and its next loads
+// do not overlap: more CTAs than that, one behind the other, keep more in flight (copying
 // 12 sequences and compacting: 890 us with 8 for both, 850 with 64 and 8, 845 with 64
-// and 16; 16 forks into 64: 400 with 6, 360 with 24). Empty CTAs cost about 0.6 us per
-// eight and SM, so a call that often has nothing to copy has few.
+// and 16; 16 forks into 64: 400 with 6, 365 with 24). Empty CTAs cost about 0.6 us per
+// eight and SM, so a call that often has nothing to copy has few. More of them resident,
+// with fewer registers: 885 us.
 constexpr int kExtendCtas = 6;
 constexpr int kCompactCtas = 8;
 constexpr int kForkCtas = 24;

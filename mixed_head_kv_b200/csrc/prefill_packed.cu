@@ -40,7 +40,7 @@
 // which a 128 x 128 tile holds about half. 12 prompts of 40 to 2500 rows, 16 query
 // heads on retrieval KV heads 72 us; 160 prompts of up to 150 rows 22 us; one of 37
 // rows 6.6 us, a chain of launch, plan, loads, two products and the output.
-// A pair of tiles takes about 3500 cycles per 128 keys, where either pipe needs 2048.
+// A pair of tiles takes about 3200 cycles per 128 keys, where either pipe needs 2048.
 // What is left is the chain of one tile (scores out of TMEM 300, weights 1950 with the
 // other tile on the same unit half of the time, handing over, 768 of products, 130
 // until the scores are seen) and the issuing warp, which cannot run ahead of the

@@ -51,6 +51,7 @@
 // exponentials gained 1 % at most.
 #include <type_traits>
 
+#include "item_queue.cuh"
 #include "paged_internal.cuh"
 #include "prefill_common.cuh"
 
@@ -129,7 +130,6 @@ constexpr int kItemFull = 21;   // + slot
 constexpr int kItemEmpty = 25;  // + slot
 constexpr int kDrain = 29;
 constexpr int kHalfDone = 32;  // + tile, one phase per first half of a product PV
-constexpr int kQueueSlots = 4;
 constexpr int kConsumers = 11;  // 8 softmax warps, the issuer, 2 V warps
 
 // Whether some row of the item's tiles sees a part only of the key tile from row0.
@@ -456,8 +456,10 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     PackItem* queue = reinterpret_cast<PackItem*>(smem + Lay::kQueue);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Lay::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kMisc + 4);
-    // By item (modulo 8): a V tile that some rows see in part held an infinity or NaN.
-    volatile int* const odd_values = reinterpret_cast<volatile int*>(smem + Lay::kMisc + 80);
+    // Marks (item_queue.cuh): a V tile that some rows of the item see in part held an
+    // infinity or NaN.
+    volatile int* const marked_odd = reinterpret_cast<volatile int*>(smem + Lay::kMisc + 80);
+    static_assert(80 + kItemMarks * 4 <= 112, "the marks end where the output rows begin");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             mbar_init(bar(kItemEmpty + s), kConsumers);
         }
         *abort_flag = 0;
-        for (int i = 0; i < 8; ++i) odd_values[i] = 0;
+        for (int i = 0; i < kItemMarks; ++i) marked_odd[i] = kNoItem;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -648,8 +650,6 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                 __syncwarp();
                 if (lane == 0) free_item(ord);
                 if (!__all_sync(0xffffffffu, more)) break;
-                // The flag of four items ago, whose rows have long been written.
-                if (half == 0 && lane == 0) odd_values[(ord + 4) & 7] = 0;
                 const int n = it.na > it.nb ? it.na : it.nb;
                 for (int j = 0; j < n; ++j, ++g) {
                     const int st = g & 1;
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                             __syncwarp();
                         }
                     }
-                    if (odd && lane == 0) odd_values[ord & 7] = 1;
+                    if (odd && lane == 0) marked_odd[mark_place(ord)] = ord;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kVFull + st));
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             const uint32_t stage = base + Lay::kStage + warp * 2048;
             const int rows = it.n - (q0 + quarter * 32);  // of the warp that exist
             bf16* const o = p.out + (static_cast<int64_t>(it.start) + q0 + quarter * 32) * p.out_stride + head * D;
-            if (odd_values[ord & 7] != 0) {
+            if (marked_odd[mark_place(ord)] == ord) {
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t r[16];

@@ -55,3 +55,29 @@ def test_prefill_scores_a_little_above_the_first_tiles_cost_what_others_do(duo, 
     fast = device_ms(lambda: c.prefill(0, start, q, flat, v, out))
     assert c.error_flags() == 0
     assert slow < 1.25 * fast, f"{slow:.3f} ms against {fast:.3f}"
+
+
+@pytest.mark.parametrize("G,D", [(1, 128), (2, 64)])
+@pytest.mark.parametrize("size", [22, 23, 24, 30, 31, 32, 33, 36, 45])
+def test_prefill_scores_of_any_size(duo, G, D, size):
+    """Scores of about 2^size, above and below zero: what a product with the scale loses to rounding is then 2^(size - 24)
+    and more, all of which the weights must not see. Keys and queries are constant rows of few bits: every score is exact
+    before the scale. Scores differ by at least 2^(size - 5) or not at all, so the weights are 0 or equal."""
+    c = duo.PagedCache(1, 2, 2 * G, 2, D, 70, 400, 16, 4, 2, [1, 0])
+    n = 900
+    gen = torch.Generator().manual_seed(size)
+    level = 1.0 + torch.randint(0, 8, (n,), generator=gen) / 8
+    level[:130] = 1.0  # (a first tile of equal scores)
+    level[500:] *= 1.5
+    sign = torch.tensor([1.0, -1.0, 0.0, 1.0])[torch.arange(n) % 4]
+    to = (size - math.log2(math.sqrt(D) * math.log2(math.e))) / 2  # D x 2^to x 2^to x the scale, in the exp2 domain
+    q = (sign * 2.0 ** round(to)).to(torch.bfloat16).view(n, 1, 1).expand(n, 2 * G, D).contiguous().cuda()
+    k = (level * 2.0 ** (size - math.floor(math.log2(math.sqrt(D) * math.log2(math.e))) - round(to))).to(torch.bfloat16).view(n, 1, 1)
+    k = k.expand(n, 2, D).contiguous().cuda()
+    v = normal(n, 2, D, seed=size)
+    out = torch.full_like(q, float("nan"))
+    c.prefill(0, ints([0, n]), q, k, v, out)
+    assert c.error_flags() == 0
+    for h in range(2):
+        ref, w = attend(q[:, h * G:h * G + G], k[:, h], v[:, h], list(range(n)), 70, 400, h == 0, 1 / math.sqrt(D))
+        check_out(out[:, h * G:h * G + G], ref, w, f"head {h}")

@@ -36,8 +36,11 @@
 //     on both sides so that a thread converts whole 16-byte words).
 //   - softmax in the exp2 domain, 32-bit statistics and sums; the maximum is
 //     moved only when a score exceeds it by more than 2^8 (exact: all terms stay
-//     relative to the same maximum). P is rounded to bf16 (f16 with E4M3): the
-//     operand type, relative error at most 2^-8 (2^-11) per term.
+//     relative to the same maximum). P is rounded to the operand type: bf16, relative
+//     error at most 2^-8 per term; with E4M3 f16, 2^-11, of weights times 2^7, the most
+//     that f16 holds when they reach 2^8: what is below 2^-21 of the maximum so far
+//     has an absolute error of 2^-32 of it instead (without the factor 2^-14 and 2^-25:
+//     beside one large key, thousands of rows weighed nothing in O and something in the sum).
 // Measured (captured launches): 4 x 131072 tokens, groups of 4, half of 8 KV heads
 // retrieval: 164 us, 6.56 TB/s, the copy rate. 32769 tokens, 8 of 32 heads
 // retrieval: 30 us, 4.6 TB/s; 48 ragged sequences of E4M3 codes 24 us; 200 of
@@ -65,6 +68,8 @@ constexpr int kPartsPerPair = 48;
 // Units of work at the end of a pair. (48 and 200 ragged sequences: 24.3 and 27.2 us; with
 // 2 units 24.5 and 26.7, with 3 25.5 and 28.0.)
 constexpr int kEndUnits = 1;
+// Weights that become f16 are 2^kLift times what they are: 2^8 x 2^7 at most, of 2^16.
+constexpr float kLift = 7.f;
 
 constexpr int kFull = 0;     // + stage (up to 6)
 constexpr int kEmpty = 6;    // + stage
@@ -849,7 +854,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             o[i][3] *= f1;
                         }
                     }
-                    const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+                    const float lift = codes ? kLift : 0.f;
+                    const float u0 = (m0 == -INFINITY ? 0.f : m0) - lift, u1 = (m1 == -INFINITY ? 0.f : m1) - lift;
                     x[0] = fast_exp2(x[0] - u0);
                     x[1] = fast_exp2(x[1] - u1);
                     x[2] = fast_exp2(x[2] - u0);

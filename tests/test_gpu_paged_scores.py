@@ -81,3 +81,41 @@ def test_prefill_scores_of_any_size(duo, G, D, size):
     for h in range(2):
         ref, w = attend(q[:, h * G:h * G + G], k[:, h], v[:, h], list(range(n)), 70, 400, h == 0, 1 / math.sqrt(D))
         check_out(out[:, h * G:h * G + G], ref, w, f"head {h}")
+
+
+# ------------------------------------------------------------------------------ decode
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (128, 8)])
+def test_decode_e4m3_many_small_weights_beside_a_large_one(duo, D, G):
+    """One key 2^25.5 above thousands of others: half of what f16 holds at its smallest. Its value row is zero, theirs are
+    one, so the output is what they weigh together, and what a warp drops shows. As many sequences as make every pair
+    lie in one share, where one warp has the large key and a quarter of the others."""
+    n, seqs, P = 6000, 150, 128
+    pages = -(-n // P)
+    c = duo.PagedCache(1, seqs, 2 * G, 2, D, 4, 16, P, pages + seqs + 1, pages + 1, [1, 1], kv_format=duo.DUO_KV_E4M3)
+    # q = 1: a key row of x in 13 columns scores 13 x scale x log2(e) above one of zeros (0 in the exp2 domain)
+    x, cols = 16.0, round(25.5 * math.sqrt(D) / (16.0 * math.log2(math.e)))
+    k, v = torch.zeros(n, 2, D, dtype=torch.bfloat16, device="cuda"), torch.ones(n, 2, D, dtype=torch.bfloat16, device="cuda")
+    k[40, :, :cols] = x
+    v[40] = 0
+    c.extend(ints([0]), ints([n]))
+    c.append(0, ints([0]), ints([0, n]), k, v)
+    c.fork(ints([0] * (seqs - 1)), ints(range(1, seqs)))
+    order = ints(range(seqs))
+    c.extend(order)
+    new_k, new_v = torch.zeros(seqs, 2, D, dtype=torch.bfloat16, device="cuda"), torch.ones(seqs, 2, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones(seqs, 2 * G, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    c.decode(0, order, q, new_k, new_v, out)
+    assert c.error_flags() == 0
+    one = torch.cat([k[:, 0], new_k[:1, 0]]), torch.cat([v[:, 0], new_v[:1, 0]])
+    ref, w = attend(q[:1, :1], *one, [n], 4, 16, True, 1 / math.sqrt(D))
+    assert 1e-5 < float(ref[0, 0, 0]) < 1e-3  # the others' part
+    # Weights rounded to f16 (2^-11), their 32-bit errors (scores below 32: exp2 of one is off by 32 x 2^-24 and its own
+    # 2^-22; sums of 6000 positive terms, 1500 in a row, by 1500 x 2^-24 at most), the output's rounding to bf16 (2^-8).
+    # In the warp with the large key the others' weights times 2^7 are f16 numbers without leading bit, in steps of
+    # 2^-24: half a step is 2^-32 of the large weight, for each of a quarter of the rows and one tile's share more.
+    tol = float(ref[0, 0, 0]) * (2.0 ** -11 + 3e-6 + 1.1e-4 + 2.0 ** -8) + (n / 4 + 128) * 2.0 ** -32
+    worst = float((out.double() - ref[0, 0, 0]).abs().max())
+    assert worst <= tol, f"{worst:.3g} of {float(ref[0, 0, 0]):.3g}"

@@ -83,6 +83,22 @@ def test_prefill_scores_of_any_size(duo, G, D, size):
         check_out(out[:, h * G:h * G + G], ref, w, f"head {h}")
 
 
+@pytest.mark.parametrize("G", [5, 6])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_other_groups(duo, G, D):
+    """Groups that no other test has: an odd one and an even one above four."""
+    c = duo.PagedCache(1, 2, 2 * G, 2, D, 4, 100, 16, 4, 2, [1, 0])
+    start = [0, 1, 130, 130, 387, 400, 1000]
+    q, k, v = (normal(1000, h, D, seed=G + h) for h in (2 * G, 2, 2))
+    out = torch.full_like(q, float("nan"))
+    c.prefill(0, ints(start), q, k, v, out)
+    assert c.error_flags() == 0
+    for a, b in zip(start, start[1:]):
+        for h in range(2):
+            ref, w = attend(q[a:b, h * G:h * G + G], k[a:b, h], v[a:b, h], list(range(b - a)), 4, 100, h == 0, 1 / math.sqrt(D))
+            check_out(out[a:b, h * G:h * G + G], ref, w, f"prompt at {a}, head {h}")
+
+
 # ------------------------------------------------------------------------------ decode
 
 
@@ -119,3 +135,51 @@ def test_decode_e4m3_many_small_weights_beside_a_large_one(duo, D, G):
     tol = float(ref[0, 0, 0]) * (2.0 ** -11 + 3e-6 + 1.1e-4 + 2.0 ** -8) + (n / 4 + 128) * 2.0 ** -32
     worst = float((out.double() - ref[0, 0, 0]).abs().max())
     assert worst <= tol, f"{worst:.3g} of {float(ref[0, 0, 0]):.3g}"
+
+
+@pytest.mark.parametrize("G", [5, 6, 8])
+def test_decode_e4m3_weights_lose_no_more_than_f16_does(duo, G):
+    """Retrieval heads of codes: f16 weights, half a step of 2^-11."""
+    c = duo.PagedCache(1, 8, 2 * G, 2, 128, 4, 60, 64, 400, 300, [1, 1], kv_format=duo.DUO_KV_E4M3)
+    scales = [[0.5, 2.0], [0.25, 1.0]]
+    c.set_kv_scales(0, *scales)
+    from paged_harness import Rows
+    rows = Rows(c)
+    lens = [3, 130, 5000]
+    for s, n in enumerate(lens):
+        k, v = normal(n, 2, 128, seed=10 * s + G), normal(n, 2, 128, seed=10 * s + G + 5)
+        c.extend(ints([s]), ints([n]))
+        c.append(0, ints([s]), ints([0, n]), k, v)
+        rows.rows[s] = (k[None], v[None])
+    q = normal(3, 2 * G, 128, seed=G)
+    out = torch.full_like(q, float("nan"))
+    last = [torch.stack([rows.rows[s][i][0, -1] for s in range(3)]) for i in (0, 1)]
+    c.decode(0, ints([0, 1, 2]), q, *last, out)
+    assert c.error_flags() == 0
+    for s, n in enumerate(lens):
+        ref, w = rows.attention(0, s, q[s:s + 1], [n - 1], 1 / math.sqrt(128), scales)
+        check_out(out[s:s + 1], ref, w, f"{n} tokens", half_p=2.0 ** -11)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_reads_every_tile(duo, fp8):
+    """Eight heads ask for one row each out of 20000, another every call: a tile that is read twice, skipped or joined
+    wrongly takes a whole output with it."""
+    n, D = 20000, 128
+    c = duo.PagedCache(1, 4, 8, 1, D, 4, 60, 64, 400, 320, [1], kv_format=duo.DUO_KV_E4M3 if fp8 else duo.DUO_KV_BF16)
+    k = torch.where(normal(n, 1, D, seed=1) > 0, 1.0, -1.0).to(torch.bfloat16)
+    v = (normal(n, 1, D, seed=2).float().clamp(-3, 3) * 4).round().div(4).to(torch.bfloat16)  # values that E4M3 holds
+    c.extend(ints([0]), ints([n]))
+    c.append(0, ints([0]), ints([0, n]), k, v)
+    out = torch.empty(1, 8, D, dtype=torch.bfloat16, device="cuda")
+    tile = 128 if fp8 else 64
+    tiles = -(-n // tile)
+    for first in range(0, tiles, 8):
+        at = [min(min(first + h, tiles - 1) * tile + (first * 5 + h * 11) % tile, n - 1) for h in range(8)]
+        q = (4 * k[at, 0]).view(1, 8, D).contiguous()
+        c.decode(0, ints([0]), q, k[n - 1:], v[n - 1:], out)
+        ref, w = attend(q, k[:, 0], v[:, 0], [n - 1], 4, 60, True, 1 / math.sqrt(D))
+        # The asked row scores 4 x 128 / 11.3 = 45, a row by chance 4 standard deviations of 4: it has all the weight.
+        assert float((ref[0] - v[at, 0].double()).abs().max()) < 1e-6
+        check_out(out, ref, w, f"rows {at}")
+    assert c.error_flags() == 0

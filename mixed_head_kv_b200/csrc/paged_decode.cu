@@ -41,6 +41,12 @@
 //     that f16 holds when they reach 2^8: what is below 2^-21 of the maximum so far
 //     has an absolute error of 2^-32 of it instead (without the factor 2^-14 and 2^-25:
 //     beside one large key, thousands of rows weighed nothing in O and something in the sum).
+//     Groups of up to four leave half of the N side free: with bf16 its columns 4 .. 7 hold
+//     the same heads again and take what the rounding left of each weight, rounded in
+//     turn. The two sums are added at the segment's end, and these groups lose 2^-16 per
+//     term, as little as the contiguous caches' groups of one and two, which multiply in
+//     32 bits (4 x 131072 tokens 165.0 us instead of 164.7, 529 tokens 7.6 instead of 7.5; for
+//     codes, whose weights lose 2^-11, the same cost 5 % and is not done).
 // Measured (captured launches): 4 x 131072 tokens, groups of 4, half of 8 KV heads
 // retrieval: 164 us, 6.56 TB/s, the copy rate. 32769 tokens, 8 of 32 heads
 // retrieval: 30 us, 4.6 TB/s; 48 ragged sequences of E4M3 codes 24 us; 200 of
@@ -112,6 +118,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+// What rounding x0 and x1 to the two numbers of `w` left, rounded too.
+__device__ __forceinline__ uint32_t bf16x2_rest(uint32_t w, float x0, float x1) {
+    return pack_bf16x2(x0 - bf16lo_to_f32(w), x1 - bf16hi_to_f32(w));
 }
 __device__ __forceinline__ void sts128(uint32_t addr, const uint4& x) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
@@ -695,15 +705,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (group_any(!ok) || s.tiles == 0) break;  // the same for all four warps
         const int g = heads[s.idx];
         const bool codes = FP8 && s.retr;  // operands are f16 made of codes
-        // The queries as the B operand: head gq, this thread's part of D.
+        const bool two_parts = p.G <= 4 && !codes;   // of each weight
+        const int head_q = two_parts ? gq & 3 : gq;  // column gq's head
+        // The queries as the B operand: column gq, this thread's part of D.
         uint32_t b[kSteps][2];
-        float scale0 = p.scale_log2, scale1 = p.scale_log2;  // of heads 2 cq and 2 cq + 1
+        float scale0 = p.scale_log2, scale1 = p.scale_log2;  // of columns 2 cq and 2 cq + 1
         if (!codes) {
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-                const uint32_t a = q + gq * D * 2 + k * 32 + cq * 4;
+                const uint32_t a = q + head_q * D * 2 + k * 32 + cq * 4;
                 b[k][0] = b[k][1] = 0u;
-                if (gq < p.G) {
+                if (head_q < p.G) {
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b[k][0]) : "r"(a));
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b[k][1]) : "r"(a + 16));
                 }
@@ -826,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             }
                         }
                     }
-                    // Rows gq and gq + 8, heads 2 cq and 2 cq + 1.
+                    // Rows gq and gq + 8, columns 2 cq and 2 cq + 1.
                     float x[4];
                     x[0] = gq < left ? (acc[0][0] + acc[1][0]) * scale0 : -INFINITY;
                     x[1] = gq < left ? (acc[0][1] + acc[1][1]) * scale1 : -INFINITY;
@@ -863,8 +875,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     l0 += x[0] + x[2];
                     l1 += x[1] + x[3];
                     // P^T from accumulator to operand layout.
-                    const uint32_t p0 = transpose8x8(codes ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]));
-                    const uint32_t p1 = transpose8x8(codes ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]));
+                    uint32_t w01 = codes ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
+                    uint32_t w23 = codes ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
+                    if (two_parts) {
+                        const uint32_t rest01 = bf16x2_rest(w01, x[0], x[1]), rest23 = bf16x2_rest(w23, x[2], x[3]);
+                        w01 = cq >= 2 ? rest01 : w01;
+                        w23 = cq >= 2 ? rest23 : w23;
+                    }
+                    const uint32_t p0 = transpose8x8(w01), p1 = transpose8x8(w23);
                     // O^T += V^T P^T
                     if (!codes) {
                         const int r = r0 + (lane & 7) + ((lane >> 4) << 3);
@@ -966,6 +984,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         else if (warp == 1) gather_quarter<1, kSteps>(o, r, merge, lane);
         else if (warp == 2) gather_quarter<2, kSteps>(o, r, merge, lane);
         else gather_quarter<3, kSteps>(o, r, merge, lane);
+        if (two_parts) {
+            // Columns 0 .. 3 take the second parts' sums from columns 4 .. 7. Where a value row
+            // has an infinity the first sum is the answer: a second part may be zero or negative.
+#pragma unroll
+            for (int i = 0; i < kSteps / kWarps; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float rest = __shfl_down_sync(0xffffffffu, r[i][j], 2);
+                    r[i][j] += isfinite(r[i][j]) ? rest : 0.f;
+                }
+        }
         const int i0 = warp * (kSteps / kWarps);
         // Column of D that accumulator i holds in its first (half 0) or second pair.
         auto col = [&](int i, int half) { return codes ? gq * (D / 8) + 2 * i + half : i * 16 + half * 8 + gq; };

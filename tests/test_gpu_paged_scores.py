@@ -137,6 +137,35 @@ def test_decode_e4m3_many_small_weights_beside_a_large_one(duo, D, G):
     assert worst <= tol, f"{worst:.3g} of {float(ref[0, 0, 0]):.3g}"
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G,D", [(1, 128), (2, 64), (2, 128), (3, 128), (4, 64), (4, 128)])
+def test_decode_small_groups_keep_their_weights(duo, G, D, fp8):
+    """Groups of up to four: bf16 weights are held in two parts, which lose 2^-16 at most (two roundings of half a step
+    each), so that only the 32-bit errors and the output's rounding are left, cut pairs and whole ones alike. Weights of
+    codes are f16: 2^-11."""
+    P, Hkv = 32, 2
+    lens = [1, 2, 5, 40, 700, 9000]
+    c = duo.PagedCache(1, 8, Hkv * G, Hkv, D, 4, 60, P, 400, 300, [1, 0], kv_format=duo.DUO_KV_E4M3 if fp8 else duo.DUO_KV_BF16)
+    scales = [[0.5, 1.0], [0.25, 1.0]]
+    if fp8:
+        c.set_kv_scales(0, *scales)
+    from paged_harness import Rows
+    rows = Rows(c)
+    for s, n in enumerate(lens):
+        k, v = normal(n, Hkv, D, seed=10 * s + G), normal(n, Hkv, D, seed=10 * s + G + 5)
+        c.extend(ints([s]), ints([n]))
+        if n > 1:
+            c.append(0, ints([s]), ints([0, n]), k, v)
+        rows.rows[s] = (k[None, :n - 1], v[None, :n - 1])
+        q = normal(1, Hkv * G, D, seed=s)
+        out = torch.full_like(q, float("nan"))
+        c.decode(0, ints([s]), q, k[n - 1:], v[n - 1:], out)
+        rows.add(s, k[None, n - 1:], v[None, n - 1:])
+        ref, w = rows.attention(0, s, q, [n - 1], 1 / math.sqrt(D), scales)
+        check_out(out, ref, w, f"{n} tokens", half_p=2.0 ** -11 if fp8 else 2.0 ** -16)
+    assert c.error_flags() == 0
+
+
 @pytest.mark.parametrize("G", [5, 6, 8])
 def test_decode_e4m3_weights_lose_no_more_than_f16_does(duo, G):
     """Retrieval heads of codes: f16 weights, half a step of 2^-11."""

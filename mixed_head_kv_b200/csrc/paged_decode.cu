@@ -57,6 +57,7 @@
 // Rows behind the last one in a page hold anything: their scores are replaced,
 // and their V rows are zeroed in shared memory (0 x NaN would not be 0).
 #include "paged_internal.cuh"
+#include "paged_shares.cuh"
 #include "sm100.cuh"
 
 namespace duo {
@@ -68,9 +69,6 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kRingBytes = 96 * 1024;
 constexpr int kMaxG = DUO_PAGED_MAX_GROUP;
-// A pair is cut into at most about this many parts: joining reads G x D floats
-// of each part in one CTA.
-constexpr int kPartsPerPair = 48;
 // Units of work at the end of a pair. (48 and 200 ragged sequences: 24.3 and 27.2 us; with
 // 2 units 24.5 and 26.7, with 3 25.5 and 28.0.)
 constexpr int kEndUnits = 1;
@@ -192,6 +190,7 @@ struct Smem {
     static constexpr int kQ = kRing + kRingBytes;
     static constexpr int kMerge = kQ + 2 * kQSlot;      // one warp's O
     static constexpr int kStat = kMerge + kMaxG * D * 4;  // maximum and sum of a warp's heads
+    static_assert(kStat % 16 == 0, "read as int4 at first");
     static constexpr int kBar = kStat + kWarps * kMaxG * 2 * 4;
     static constexpr int kMisc = kBar + 32 * 8;
     static constexpr int kSeg = kMisc + 16;     // the two segments in flight, and two cut pairs to be joined
@@ -449,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
     }
     __syncthreads();
-    int sum_r = 0, sum_s = 0;
+    int sum_r = 0, sum_s = 0, longest = 0;  // units; of the longest pair
     bool wrong = false;
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
@@ -467,8 +466,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             seq_of[i0 + j] = static_cast<uint16_t>(s < 0 ? 0 : s);
         }
         if (my_len[j] > 0) {  // tiles, and the end of the pair
-            sum_r += (my_len[j] + kPageTile - 1) / kPageTile + kEndUnits;
-            sum_s += ((my_len[j] < v.W ? my_len[j] : v.W) + kWinTile - 1) / kWinTile + kEndUnits;
+            const int units_r = (my_len[j] + kPageTile - 1) / kPageTile + kEndUnits;
+            const int units_s = ((my_len[j] < v.W ? my_len[j] : v.W) + kWinTile - 1) / kWinTile + kEndUnits;
+            sum_r += units_r;
+            sum_s += units_s;
+            if (p.h.n_retr > 0) longest = max(longest, units_r);
+            if (p.h.n_strm > 0) longest = max(longest, units_s);
         }
     }
     if (wrong && blockIdx.x == 0) report(v.err, kErrPagedArgument);
@@ -480,14 +483,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         sum_r += lane >= o ? x : 0;
         sum_s += lane >= o ? y : 0;
     }
-    int2* const of_warp = reinterpret_cast<int2*>(smem + L::kStat);
-    if (lane == 31) of_warp[warp] = make_int2(sum_r, sum_s);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    int4* const of_warp = reinterpret_cast<int4*>(smem + L::kStat);
+    if (lane == 31) of_warp[warp] = make_int4(sum_r, sum_s, longest, 0);
     fence_proxy_async_smem();  // the marks' words become TMA destinations
     __syncthreads();
     int total_r = 0, total_s = 0, off_r = sum_r - own_r, off_s = sum_s - own_s;
 #pragma unroll
     for (int w = 0; w <= kWarps; ++w) {
-        const int2 x = of_warp[w];
+        const int4 x = of_warp[w];
+        longest = max(longest, x.z);
         off_r += w < warp ? x.x : 0;
         off_s += w < warp ? x.y : 0;
         total_r += x.x;
@@ -520,10 +525,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     work.n_strm = p.h.n_strm;
     work.of_retr = static_cast<int64_t>(total_r) * p.h.n_retr;
     const int64_t total = work.of_retr + static_cast<int64_t>(total_s) * p.h.n_strm;
-    const int64_t pairs = static_cast<int64_t>(p.n) * (p.h.n_retr + p.h.n_strm);
-    int n_cta = gridDim.x;
-    if (n_cta > total) n_cta = static_cast<int>(total);
-    if (n_cta > pairs * kPartsPerPair) n_cta = static_cast<int>(pairs * kPartsPerPair);
+    const int n_cta = share_count(total, longest, gridDim.x);
     const int c = blockIdx.x;
     if (c >= n_cta) return;
     Segment* const slots = reinterpret_cast<Segment*>(smem + L::kSeg);

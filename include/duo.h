@@ -448,8 +448,9 @@ DUO_API duo_status duo_paged_extend(duo_paged* cache, int32_t n, const int32_t* 
  * sequence seqs[i], in order (duo_paged_extend comes first). n_rows: rows of the
  * k and v tensors; rows outside every range are not read. Slots as in
  * duo_cache_append. An entry whose range is not within [0, n_rows], is longer
- * than the sequence or runs backwards is skipped (DUO_ERR_BIT_PAGED_ARGUMENT); a
- * row that would go into a page shared with another sequence is not written
+ * than the sequence or runs backwards is skipped (DUO_ERR_BIT_PAGED_ARGUMENT;
+ * ranges behind it may then overlap others, and a call whose ranges hold more than
+ * 2^30 tokens in all appends nothing); a row that would go into a page shared with another sequence is not written
  * (DUO_ERR_BIT_PAGED_SHARED: it would change that sequence too). */
 DUO_API duo_status duo_paged_append(duo_paged* cache, int32_t layer, int32_t n, const int32_t* seqs,
                                     const int32_t* row_start, const void* k, const void* v, int64_t n_rows,

@@ -340,7 +340,7 @@ duo_status duo_paged_append(duo_paged* c, int32_t layer, int32_t n, const int32_
     p.n = n;
     p.fp8 = c->fp8 ? 1 : 0;
     p.kv_scale = scales_of(c, layer);
-    return launch_paged_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DUO_OK : DUO_ERR_CUDA;
+    return launch_paged_append(p, c->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DUO_OK : DUO_ERR_CUDA;
 }
 
 duo_status duo_paged_prefill(duo_paged* c, int32_t layer, int32_t n, const int32_t* row_start, const void* q,

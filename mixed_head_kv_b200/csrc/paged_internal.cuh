@@ -89,7 +89,7 @@ struct PagedAppendParams {
     int32_t n, fp8;
     const float* kv_scale;  // fp8: [Hkv][k_scale, v_scale, 1/k_scale, 1/v_scale]
 };
-cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendParams& p, int num_sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ decode
 struct PagedDecodeParams {

@@ -471,6 +471,8 @@ class PagedCache:
     between rows is free (a slice of a fused projection), a row itself is dense. A step is: extend once, then per layer
     prefill + append (whole prompts) or decode (one token). Calls run on the current stream and must be ordered among
     themselves; nothing waits for the device except error_flags. A captured CUDA graph of a step may be replayed.
+    `stream`: where the cache is set up, behind what the current stream holds by then. A cache that was used on other
+    streams than that one (or in a graph) is closed, or dropped, when their work has ended.
     """
 
     _NAMES = ("k_pages", "v_pages", "k_window", "v_window", "page_table", "seq_len", "page_ref")
@@ -512,11 +514,18 @@ class PagedCache:
             raise ValueError("a paged cache lives on a CUDA device")
         self._workspace = torch.empty(sizes.workspace, dtype=torch.uint8, device=self.device)
         buffers.workspace = self._workspace.data_ptr()
+        self._constants()
         with torch.cuda.device(self.device):
-            st, handle = duo_paged_alloc(self.layout, mask, buffers, stream)
+            here, raw = torch.cuda.current_stream(), _stream(stream)
+            if raw != here.cuda_stream:  # the tensors are allocated and filled on the current stream
+                other = torch.cuda.ExternalStream(raw) if isinstance(stream, int) else stream
+                other.wait_stream(here)
+                if not isinstance(stream, int):
+                    for t in (self._workspace, *(tensors[n] for n in self._NAMES)):
+                        t.record_stream(other)
+            st, handle = duo_paged_alloc(self.layout, mask, buffers, raw)
         _check(st, "duo_paged_alloc")
         self.handle = handle
-        self._constants()
 
     def _constants(self):
         """What the argument checks compare with on every call."""
@@ -580,7 +589,7 @@ class PagedCache:
         heads = self.layout.num_kv_heads
         if len(k_scale) != heads or len(v_scale) != heads:
             raise ValueError(f"expected {heads} scales for k and for v")
-        _check(duo_paged_set_kv_scales(self.handle, layer, k_scale, v_scale, stream), "duo_paged_set_kv_scales")
+        _check(duo_paged_set_kv_scales(self.handle, layer, k_scale, v_scale, self._on(stream)), "duo_paged_set_kv_scales")
 
     def extend(self, seqs, n_tok=None, stream=None):
         """Sequence seqs[i] gets n_tok[i] (default 1) more tokens."""
@@ -643,6 +652,6 @@ class PagedCache:
         _check(_lib.duo_paged_compact(self.handle, self._on(stream)), "duo_paged_compact")
 
     def error_flags(self, stream=None) -> int:
-        st, f = duo_paged_error(self.handle, stream)
+        st, f = duo_paged_error(self.handle, self._on(stream))
         _check(st, "duo_paged_error")
         return f

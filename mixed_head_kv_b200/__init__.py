@@ -306,6 +306,8 @@ def make_paged_layout(num_layers, max_seqs, num_q_heads, num_kv_heads, head_dim,
 def duo_paged_size(layout: duo_paged_layout, is_retrieval: Sequence[int]):
     """(status, duo_paged_sizes): bytes of each device buffer."""
     sizes = duo_paged_sizes()
+    if len(is_retrieval) < layout.num_layers * layout.num_kv_heads:  # the library reads that many
+        return DUO_ERR_INVALID_ARG, sizes
     st = _lib.duo_paged_size(ctypes.byref(layout), ctypes.cast(_mask_buf(is_retrieval), _P), ctypes.byref(sizes))
     return st, sizes
 
@@ -313,6 +315,8 @@ def duo_paged_size(layout: duo_paged_layout, is_retrieval: Sequence[int]):
 def duo_paged_alloc(layout: duo_paged_layout, is_retrieval: Sequence[int], buffers: duo_paged_buffers, stream=None):
     """(status, handle)."""
     handle = _P()
+    if len(is_retrieval) < layout.num_layers * layout.num_kv_heads:
+        return DUO_ERR_INVALID_ARG, None
     st = _lib.duo_paged_alloc(ctypes.byref(layout), ctypes.cast(_mask_buf(is_retrieval), _P), ctypes.byref(buffers),
                               _stream(stream), ctypes.byref(handle))
     return st, handle.value

@@ -510,8 +510,18 @@ DUO_API duo_status duo_paged_compact(duo_paged* cache, void* stream);
 #define DUO_ERR_BIT_PAGED_CAPACITY 8u  /* too few free pages, or more than max_pages for a sequence */
 #define DUO_ERR_BIT_PAGED_SHARED 16u   /* a write to a shared page was left out */
 #define DUO_ERR_BIT_PAGED_WAIT 32u     /* a bounded wait of a kernel ran out: the outputs since then are not
-                                        * valid, and a new duo_paged over the same buffers is needed */
+                                        * valid, and a new duo_paged over the same buffers is needed, with
+                                        * which the step's prefill and decode calls can be made again */
 DUO_API duo_status duo_paged_error(duo_paged* cache, void* stream, uint32_t* flags);
+
+/* duo_paged_test_wait_timeout — as duo_cache_test_wait_timeout, for the next
+ * duo_paged_decode (DUO_TEST_WAIT_DECODE) or duo_paged_prefill
+ * (DUO_TEST_WAIT_PREFILL) launch that has work: its first CTA issues no K and V
+ * tile, and the waits for them run out after the usual second. Error bit
+ * DUO_ERR_BIT_PAGED_WAIT; the outputs of that CTA's share (decode), or of its
+ * first work item (prefill), are wrong or not written, all others are right.
+ * 0 disarms. DUO_ERR_INVALID_ARG for an unknown kind. */
+DUO_API duo_status duo_paged_test_wait_timeout(duo_paged* cache, int32_t launches);
 
 /* duo_status_str — static description of a status code. */
 DUO_API const char* duo_status_str(duo_status status);

@@ -50,7 +50,7 @@ EXPORTED = ("duo_cache_alloc", "duo_cache_free", "duo_cache_append", "duo_prefil
             "duo_cache_test_wait_timeout",
             "duo_paged_size", "duo_paged_alloc", "duo_paged_free", "duo_paged_set_kv_scales", "duo_paged_extend",
             "duo_paged_append", "duo_paged_prefill", "duo_paged_decode", "duo_paged_fork", "duo_paged_copy",
-            "duo_paged_release", "duo_paged_compact", "duo_paged_error")
+            "duo_paged_release", "duo_paged_compact", "duo_paged_error", "duo_paged_test_wait_timeout")
 DUO_PAGED_MAX_SEQS = 4096  # paged caches (include/duo.h)
 DUO_PAGED_MAX_BATCH = 512
 DUO_PAGED_MAX_GROUP = 8
@@ -153,6 +153,8 @@ _lib.duo_paged_release.restype = _ST
 _lib.duo_paged_release.argtypes = [_P, _I32, _P, _P]
 _lib.duo_paged_compact.restype = _ST
 _lib.duo_paged_compact.argtypes = [_P, _P]
+_lib.duo_paged_test_wait_timeout.restype = _ST
+_lib.duo_paged_test_wait_timeout.argtypes = [_P, _I32]
 _lib.duo_paged_error.restype = _ST
 _lib.duo_paged_error.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint32)]
 
@@ -367,6 +369,11 @@ def duo_paged_release(handle, n, seqs, stream=None) -> int:
 
 def duo_paged_compact(handle, stream=None) -> int:
     return _lib.duo_paged_compact(handle, _stream(stream))
+
+
+def duo_paged_test_wait_timeout(handle, launches: int) -> int:
+    """Arm the next launch of the given kinds to test the bounded waits (include/duo.h)."""
+    return _lib.duo_paged_test_wait_timeout(handle, launches)
 
 
 def duo_paged_error(handle, stream=None):

@@ -379,6 +379,8 @@ duo_status duo_paged_prefill(duo_paged* c, int32_t layer, int32_t n, const int32
     p.R = L.recent;
     p.scale_log2 = c->scale * 1.4426950408889634f;
     p.h = c->heads[layer];
+    p.test_withhold = (c->test_wait & DUO_TEST_WAIT_PREFILL) ? 1 : 0;  // one launch only
+    c->test_wait &= ~DUO_TEST_WAIT_PREFILL;
     return launch_prefill_packed(p, m, c->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DUO_OK : DUO_ERR_CUDA;
 }
 
@@ -412,9 +414,17 @@ duo_status duo_paged_decode(duo_paged* c, int32_t layer, int32_t n, const int32_
     p.part_o = c->part_o;
     p.part_ml = c->part_ml;
     p.counters = c->counters;
+    p.test_withhold = (c->test_wait & DUO_TEST_WAIT_DECODE) ? 1 : 0;  // one launch only
+    c->test_wait &= ~DUO_TEST_WAIT_DECODE;
     return launch_paged_decode(p, c->maps, c->fp8 ? 1 : 0, c->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? DUO_OK
                : DUO_ERR_CUDA;
+}
+
+duo_status duo_paged_test_wait_timeout(duo_paged* c, int32_t launches) {
+    if (!c || (launches & ~(DUO_TEST_WAIT_DECODE | DUO_TEST_WAIT_PREFILL)) != 0) return DUO_ERR_INVALID_ARG;
+    c->test_wait = launches;
+    return DUO_OK;
 }
 
 duo_status duo_paged_error(duo_paged* c, void* stream, uint32_t* flags) {

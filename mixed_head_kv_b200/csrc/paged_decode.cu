@@ -589,7 +589,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 slots[slot] = s;
                 mbar_arrive(bar(kQFull + slot));  // releases the segment
             }
-            for (int t = s.t0; t < s.t1; ++t) {
+            if (p.test_withhold != 0 && c == 0) {  // a test of the waits for these tiles: none is loaded
+                mbar_wait(bar(kEmpty), 0, abort_flag, 2 * kWaitTimeoutNs);
+                ok = false;
+            }
+            for (int t = s.t0; ok && t < s.t1; ++t) {
                 if (round > 0 && !mbar_wait(bar(kEmpty + st), (round - 1) & 1, abort_flag)) {
                     ok = false;
                     break;

@@ -107,6 +107,7 @@ struct PagedDecodeParams {
     float* part_o;       // [kPagedMaxCtas][2][G][D]
     float* part_ml;      // [kPagedMaxCtas][2][G][2] running maximum and sum
     uint32_t* counters;  // [kPagedMaxBatch * Hkv], zero between launches
+    int32_t test_withhold;  // 1: a test of the bounded waits (duo_paged_test_wait_timeout)
 };
 struct PagedMaps {
     CUtensorMap k, v;    // pages (D, P, num_pages * R)
@@ -125,6 +126,7 @@ struct PackedPrefillParams {
     int64_t n_rows, out_stride;
     int32_t n, Hq, Hkv, G, D, S, R;
     float scale_log2;
+    int32_t test_withhold;  // 1: a test of the bounded waits (duo_paged_test_wait_timeout)
     PagedHeads h;
 };
 struct PackedMaps {
@@ -147,6 +149,7 @@ struct duo_paged {
     int device = 0;
     int num_sms = 148;
     bool fp8 = false;
+    int32_t test_wait = 0;               // duo_paged_test_wait_timeout: launch kinds still to withhold tiles
     duo::PagedView view{};
     std::vector<duo::PagedHeads> heads;  // [layers]
     duo::PagedMaps maps{};

@@ -605,6 +605,11 @@ __global__ void __launch_bounds__(kPackThreads, 1)
                                     it.start + it.qb);
                 }
                 ++q_loads;
+                if (p.test_withhold != 0 && blockIdx.x == 0) {  // a test of the waits for the tiles: none is loaded
+                    mbar_wait(bar(kKEmpty), 0, abort_flag, 2 * kWaitTimeoutNs);
+                    ok = false;
+                    break;
+                }
                 // K and V tiles in turn: by the time a K stage is free the V stage before it is.
                 const int n = it.na > it.nb ? it.na : it.nb;
 #pragma unroll 1

@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
             }
             if (owner) {
+                if (!ok && new_page >= 0 && new_page < v.num_pages) new_ref = v.ref[new_page];  // perhaps not looked at yet
                 if (!s.retr) {
                     bf16* dst = (which ? v.v_window : v.k_window) +
                                 ((static_cast<int64_t>(s.seq) * v.s_all + p.h.s0 + s.idx - p.h.n_retr) * v.W + new_row) * D + ch * 8;

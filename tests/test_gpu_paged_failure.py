@@ -81,6 +81,23 @@ def test_decode_wait_runs_out(duo, D, G, fp8):
     assert c.error_flags() == 0
 
 
+def test_a_shared_page_is_not_written_after_a_wait_ran_out(duo):
+    """The CTA that gives up before its first tile still has the new row to store: not into a page that is shared."""
+    c = duo.PagedCache(1, 4, 4, 2, 64, 4, 60, 32, 8, 4, [1, 0])
+    c.extend(ints([0]), ints([20]))
+    k, v = normal(20, 2, 64, seed=1), normal(20, 2, 64, seed=2)
+    c.append(0, ints([0]), ints([0, 20]), k, v)
+    c.fork(ints([0]), ints([1]))
+    held = [t.clone() for t in (c.k_pages, c.v_pages)]
+    q, k1, v1 = (normal(1, h, 64, seed=3 + h) for h in (4, 2, 2))
+    assert c.error_flags() == 0
+    duo.duo_paged_test_wait_timeout(c.handle, duo.DUO_TEST_WAIT_DECODE)
+    c.decode(0, ints([0]), q, k1, v1, torch.empty_like(q))
+    assert flags_within(c, 8) == duo.DUO_ERR_BIT_PAGED_WAIT | duo.DUO_ERR_BIT_PAGED_SHARED
+    for t, h in zip((c.k_pages, c.v_pages), held):
+        assert torch.equal(t.view(torch.int16), h.view(torch.int16))
+
+
 @pytest.mark.parametrize("D,G", [(64, 1), (128, 2)])
 def test_prefill_wait_runs_out(duo, D, G):
     c = duo.PagedCache(1, 4, 2 * G, 2, D, 4, 100, 16, 4, 2, [1, 0])

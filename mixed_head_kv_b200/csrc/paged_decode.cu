@@ -48,9 +48,9 @@
 //     32 bits (4 x 131072 tokens 165.0 us instead of 164.7, 529 tokens 7.6 instead of 7.5; for
 //     codes, whose weights lose 2^-11, the same cost 5 % and is not done).
 // Measured (captured launches): 4 x 131072 tokens, groups of 4, half of 8 KV heads
-// retrieval: 164 us, 6.56 TB/s, the copy rate. 32769 tokens, 8 of 32 heads
-// retrieval: 30 us, 4.6 TB/s; 48 ragged sequences of E4M3 codes 24 us; 200 of
-// groups of 8 27 us; 529 tokens 7.8 us. What the smaller ones take beyond the
+// retrieval: 165 us, 6.53 TB/s, the copy rate. 32769 tokens, 8 of 32 heads
+// retrieval: 30.5 us, 4.5 TB/s; 48 ragged sequences of E4M3 codes 22 us; 200 of
+// groups of 8 23.5 us; 529 tokens 7.7 us. What the smaller ones take beyond the
 // bytes is fixed: about 3 us until the first tiles arrive (lengths, the sums over
 // the entries, page numbers, rows: a chain of loads), 2 us at each pair's end and
 // 4 us for counting and joining.
@@ -69,8 +69,8 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kRingBytes = 96 * 1024;
 constexpr int kMaxG = DUO_PAGED_MAX_GROUP;
-// Units of work at the end of a pair. (48 and 200 ragged sequences: 24.3 and 27.2 us; with
-// 2 units 24.5 and 26.7, with 3 25.5 and 28.0.)
+// Units of work at the end of a pair. (48 and 200 ragged sequences, outside a captured
+// launch: 24.3 and 27.2 us; with 2 units 24.5 and 26.7, with 3 25.5 and 28.0.)
 constexpr int kEndUnits = 1;
 // Weights that become f16 are 2^kLift times what they are: 2^8 x 2^7 at most, of 2^16.
 constexpr float kLift = 7.f;

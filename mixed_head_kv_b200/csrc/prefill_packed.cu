@@ -35,11 +35,11 @@
 // (relative 2^-8 at most per term). Every mbarrier wait is bounded; on timeout the
 // CTA records kErrPagedWait and unwinds.
 //
-// Measured: 32768 rows, D = 128: 8 retrieval heads 1.65 ms, 1330 TFLOP/s; 24
-// streaming heads (sink 64, recent 256) 0.26 ms, 490 TFLOP/s of unmasked pairs, of
+// Measured: 32768 rows, D = 128: 8 retrieval heads 1.68 ms, 1310 TFLOP/s; 24
+// streaming heads (sink 64, recent 256) 0.28 ms, 460 TFLOP/s of unmasked pairs, of
 // which a 128 x 128 tile holds about half. 12 prompts of 40 to 2500 rows, 16 query
-// heads on retrieval KV heads 72 us; 160 prompts of up to 150 rows 22 us; one of 37
-// rows 6.6 us, a chain of launch, plan, loads, two products and the output.
+// heads on retrieval KV heads 75 us; 160 prompts of up to 150 rows 21.6 us; one of 37
+// rows 6.4 us, a chain of launch, plan, loads, two products and the output.
 // A pair of tiles takes about 3200 cycles per 128 keys, where either pipe needs 2048.
 // What is left is the chain of one tile (scores out of TMEM 300, weights 1950 with the
 // other tile on the same unit half of the time, handing over, 768 of products, 130

@@ -873,12 +873,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             o[i][3] *= f1;
                         }
                     }
-                    const float lift = codes ? kLift : 0.f;
-                    const float u0 = (m0 == -INFINITY ? 0.f : m0) - lift, u1 = (m1 == -INFINITY ? 0.f : m1) - lift;
-                    x[0] = fast_exp2(x[0] - u0);
-                    x[1] = fast_exp2(x[1] - u1);
-                    x[2] = fast_exp2(x[2] - u0);
-                    x[3] = fast_exp2(x[3] - u1);
+                    const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+                    x[0] -= u0;
+                    x[1] -= u1;
+                    x[2] -= u0;
+                    x[3] -= u1;
+                    if (codes) {  // to the difference: a large maximum less kLift would be rounded
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] += kLift;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = fast_exp2(x[i]);
                     l0 += x[0] + x[2];
                     l1 += x[1] + x[3];
                     // P^T from accumulator to operand layout.

@@ -31,9 +31,9 @@
 // it was made from, O of A and of B at 256.
 // Softmax in the exp2 domain; the running maximum moves when a score exceeds it by more
 // than 2^8, and to any higher score once 64 weights have added up to more than 2^10
-// (exact: all terms stay relative to the same maximum), sums in 32 bits; P rounded to bf16, the operand type
-// (relative 2^-8 at most per term). Every mbarrier wait is bounded; on timeout the
-// CTA records kErrPagedWait and unwinds.
+// (exact: all terms stay relative to the same maximum), sums in 32 bits; P rounded to
+// bf16, the operand type (relative 2^-8 at most per term). Every mbarrier wait is bounded;
+// on timeout the CTA records kErrPagedWait and unwinds.
 //
 // Measured: 32768 rows, D = 128: 8 retrieval heads 1.68 ms, 1310 TFLOP/s; 24
 // streaming heads (sink 64, recent 256) 0.28 ms, 460 TFLOP/s of unmasked pairs, of

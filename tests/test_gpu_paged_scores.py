@@ -138,6 +138,48 @@ def test_decode_e4m3_many_small_weights_beside_a_large_one(duo, D, G):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G,D", [(1, 128), (8, 64)])
+@pytest.mark.parametrize("size", [0, 20, 24, 25, 26, 27, 30, 32, 40])
+def test_decode_scores_of_any_size(duo, G, D, size, fp8):
+    """Scores of about 2^size that differ by 2^(size - 5) or not at all (weights 0 or equal), then value rows of ones with
+    scores that differ by as little as 32 bits show: whatever the weights are, they divide by their sum."""
+    n = 3000
+    c = duo.PagedCache(1, 2, 2 * G, 2, D, 4, 60, 32, 100, 96, [1, 0], kv_format=duo.DUO_KV_E4M3 if fp8 else duo.DUO_KV_BF16)
+    from paged_harness import Rows
+    rows, gen = Rows(c), torch.Generator().manual_seed(size)
+    level = 1.0 + torch.randint(0, 8, (n,), generator=gen) / 8
+    level[:500] = 1.0
+    level[n // 2:] *= 2
+    k = level.to(torch.bfloat16).view(n, 1, 1).expand(n, 2, D).contiguous().cuda()
+    v = normal(n, 2, D, seed=size)
+    scales = [[1.0, 1.0], [1.0, 1.0]]
+    c.extend(ints([0]), ints([n]))
+    c.append(0, ints([0]), ints([0, n]), k, v)
+    rows.rows[0] = (k[None], v[None])
+    factor = 2.0 ** (size - round(math.log2(math.sqrt(D) * math.log2(math.e))))
+    out = torch.empty(1, 2 * G, D, dtype=torch.bfloat16, device="cuda")
+    if size > 9:
+        for sign in (1.0, -1.0):
+            q = torch.full((1, 2 * G, D), sign * factor, dtype=torch.bfloat16, device="cuda")
+            c.decode(0, ints([0]), q, k[n - 1:], v[n - 1:], out)
+            ref, w = rows.attention(0, 0, q, [n - 1], 1 / math.sqrt(D), scales)
+            check_out(out, ref, w, f"sign {sign}")
+    # Half of the columns give all rows the same large score, one column up to 15 units of 2^-23 of it more: a difference of
+    # 2^8 between weights, the most that the maximum does not follow, is one or two such units from size 25 on.
+    k = torch.ones(n, 2, D, dtype=torch.bfloat16, device="cuda")
+    k[:, :, -1] = (torch.randint(0, 16, (n, 1), generator=gen)).to(k)
+    k[:64, :, -1] = 0
+    k[64:2000, :, -1].clamp_(max=1)
+    c.append(0, ints([0]), ints([0, n]), k, torch.ones_like(k))
+    q = torch.zeros(1, 2 * G, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, :D // 2] = factor
+    q[:, :, -1] = factor * D * 2.0 ** -24
+    c.decode(0, ints([0]), q, k[n - 1:], torch.ones_like(k[:1]), out)
+    assert float((out.double() - 1).abs().max()) <= 2.0 ** -8 + 4e-4 + 2.0 ** -8
+    assert c.error_flags() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("G,D", [(1, 128), (2, 64), (2, 128), (3, 128), (4, 64), (4, 128)])
 def test_decode_small_groups_keep_their_weights(duo, G, D, fp8):
     """Groups of up to four: bf16 weights are held in two parts, which lose 2^-16 at most (two roundings of half a step

@@ -101,3 +101,37 @@ def test_more_tokens_than_32_bits_hold_are_refused(duo):
     c.append(0, ints(range(64)), ints([0, n] * 32 + [0]), rows, rows)
     assert c.error_flags() == duo.DUO_ERR_BIT_PAGED_ARGUMENT
     assert (c.k_window == 3).all() and (c.v_window == 3).all()
+
+
+def test_captured_append_follows_its_entries(duo):
+    """One captured extend and append, replayed with other sequences, counts and rows."""
+    c = duo.PagedCache(1, 8, 2, 2, 64, 4, 20, 16, 60, 20, [1, 0])
+    poison(c)
+    model, rows = Model(60, 16, 20, 8), Rows(c)
+    seqs, n_tok, start = ints([0] * 4), ints([0] * 4), ints([0] * 5)
+    k, v = normal(200, 2, 64, seed=1), normal(200, 2, 64, seed=2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            c.extend(seqs, n_tok)
+            c.append(0, seqs, start, k, v)
+    torch.cuda.current_stream().wait_stream(side)
+    for turn, (s, n) in enumerate((([3, 1, 7, -1], [150, 1, 0, 9]), ([0, 3, 9, 1], [1, 1, 5, 190]), ([5, -1, -1, 3], [17, 1, 1, 16]))):
+        live = [(a, b) for a, b in zip(s, n) if 0 <= a < 8]
+        assert model.extend([a for a, _ in live], [b for _, b in live])
+        at = [0]
+        for b in n:
+            at.append(at[-1] + b)
+        for t, x in ((seqs, s), (n_tok, n), (start, at)):
+            t.copy_(ints(x))
+        k.copy_(normal(200, 2, 64, seed=10 + turn))
+        v.copy_(normal(200, 2, 64, seed=20 + turn))
+        graph.replay()
+        for i, a in enumerate(s):
+            if 0 <= a < 8:
+                rows.add(a, k[None, at[i]:at[i + 1]].clone(), v[None, at[i]:at[i + 1]].clone())
+    model.check(c)
+    rows.check(model)
+    assert c.error_flags() == 0

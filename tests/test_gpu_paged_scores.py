@@ -254,3 +254,21 @@ def test_decode_reads_every_tile(duo, fp8):
         assert float((ref[0] - v[at, 0].double()).abs().max()) < 1e-6
         check_out(out, ref, w, f"rows {at}")
     assert c.error_flags() == 0
+
+
+@pytest.mark.parametrize("scale", [0.01, 0.4])
+def test_a_softmax_scale_of_the_callers(duo, scale):
+    """Prompts and steps with another scale than 1 / sqrt(head_dim)."""
+    c = duo.PagedCache(1, 4, 6, 2, 64, 4, 60, 16, 40, 20, [1, 0], softmax_scale=scale)
+    n = 200
+    q, k, v = (normal(n + 1, h, 64, seed=h) for h in (6, 2, 2))
+    out = torch.full_like(q, float("nan"))
+    c.extend(ints([2]), ints([n]))
+    c.prefill(0, ints([0, n]), q[:n], k[:n], v[:n], out[:n])
+    c.append(0, ints([2]), ints([0, n]), k, v)
+    c.extend(ints([2]))
+    c.decode(0, ints([2]), q[n:], k[n:], v[n:], out[n:])
+    for h in range(2):
+        ref, w = attend(q[:, h * 3:h * 3 + 3], k[:, h], v[:, h], list(range(n + 1)), 4, 60, h == 0, scale)
+        check_out(out[:, h * 3:h * 3 + 3], ref, w, f"head {h}")
+    assert c.error_flags() == 0
